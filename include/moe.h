@@ -60,8 +60,10 @@ typedef enum {
     MOE_ESCRATCH = -5       /* moe_layer_forward_static: the call needs more than its static buffer */
 } moe_status;
 
-/* Element type of the activations x [T][d_model], row-major. */
-typedef enum { MOE_X_F32 = 0, MOE_X_BF16 = 1 } moe_xtype;
+/* Element type of the activations x [T][d_model], row-major.  MOE_X_MX4 (rows of MX4 codes with
+ * their scales, see moe_quantize_rows_mx4) is taken by moe_matmul_mx4 only, MOE_X_F64 by the
+ * logits of moe_balance_loss and moe_balance_loss_backward only. */
+typedef enum { MOE_X_F32 = 0, MOE_X_BF16 = 1, MOE_X_MX4 = 2, MOE_X_F64 = 3 } moe_xtype;
 
 /* Expert weight formats.
  *  MOE_W_Q8_0:   blocks of 32 int8 values along the reduction dimension K with one fp16 scale
@@ -77,14 +79,21 @@ typedef enum { MOE_X_F32 = 0, MOE_X_BF16 = 1 } moe_xtype;
  *                magnitude 448) with one fp32 scale per output row, value = e4m3(q) * scale; the
  *                same arrays as MOE_W_I8_ROW.  Runs only with MOE_F_PREFILL_FP8.  The
  *                Inferentia page's fp4 section names INT8 and FP8 as the two quantised types its
- *                inference stack runs; this is the FP8 one at the per-row granularity. */
+ *                inference stack runs; this is the FP8 one at the per-row granularity.
+ *  MOE_W_MX4:    MXFP4 of the OCP Microscaling Formats specification v1.0: E2M1 codes, two per
+ *                byte with element 2i in the low nibble, and one E8M0 scale byte s per 32 contiguous
+ *                values along the reduction dimension, value = e2m1(q) * 2^(s - 127); s = 0xFF makes
+ *                the block NaN.  Both matrices row-major.  d_ff a multiple of 64.  Without a flag x
+ *                and h enter exactly; with MOE_F_PREFILL_MX4 they are quantised to MX4 too. */
 typedef enum {
     MOE_W_Q8_0 = 0, MOE_W_I8_ROW = 1, MOE_W_E2M1_G16 = 2,
     MOE_W_Q8_0_TILED = 3, MOE_W_I8_ROW_TILED = 4,  /* same values, tiled layout (below) */
-    MOE_W_FP8_ROW = 5, MOE_W_FP8_ROW_TILED = 6
+    MOE_W_FP8_ROW = 5, MOE_W_FP8_ROW_TILED = 6,
+    MOE_W_MX4 = 8
 } moe_wformat;
 
-typedef enum { MOE_ACT_SWIGLU = 0, MOE_ACT_RELU2 = 1 } moe_act;
+/* MOE_ACT_NONE (the product itself) is taken by moe_matmul_mx4 only. */
+typedef enum { MOE_ACT_SWIGLU = 0, MOE_ACT_RELU2 = 1, MOE_ACT_NONE = 2 } moe_act;
 
 enum {
     /* E2M1 experts: the down projection reads only 16-neuron groups of h holding a nonzero
@@ -104,22 +113,27 @@ enum {
      * moe_quantize_rows_fp8).  Both projections are E4M3 x E4M3 products (each exact in fp32)
      * summed in fp32 on the matrix cores, then rescaled by the two row scales.  Not combinable
      * with MOE_F_PREFILL_I8 (MOE_EINVAL). */
-    MOE_F_PREFILL_FP8 = 8u
+    MOE_F_PREFILL_FP8 = 8u,
+    /* MX4 experts only (SwiGLU or ReLU^2): the batched-prefill definition in MX4.  x per token and
+     * h per pair are quantised as moe_quantize_rows_mx4 does, h from its fp32 value; both
+     * projections are MX4 x MX4 products summed in fp32 on the matrix cores.  Not combinable with
+     * the other prefill flags (MOE_EINVAL). */
+    MOE_F_PREFILL_MX4 = 16u
 };
 
 /*
  * The E experts of one layer.  rows = 2*d_ff for SwiGLU (gate rows 0..d_ff-1, then up rows),
  * d_ff for ReLU^2 (up rows only).
  *   gate_up:        Q8_0 / I8_ROW: int8 [E][rows][d_model];  E2M1: uint8 [E][rows][d_model/2];
- *                   FP8_ROW: uint8 E4M3 [E][rows][d_model]
+ *                   FP8_ROW: uint8 E4M3 [E][rows][d_model];  MX4: uint8 [E][rows][d_model/2]
  *   gate_up_scales: Q8_0: fp16 [E][rows][d_model/32];  I8_ROW / FP8_ROW: fp32 [E][rows];
- *                   E2M1: fp16 [E][rows][d_model/16]
+ *                   E2M1: fp16 [E][rows][d_model/16];  MX4: uint8 [E][rows][d_model/32]
  *   down:           Q8_0 / I8_ROW: int8 [E][d_model][d_ff];  FP8_ROW: uint8 E4M3 [E][d_model][d_ff];
  *                   E2M1: neuron-major uint8 [E][d_ff][d_model/2] (neuron f's d_model codes
- *                   contiguous, output 2i in the low nibble)
+ *                   contiguous, output 2i in the low nibble);  MX4: uint8 [E][d_model][d_ff/2]
  *   down_scales:    Q8_0: fp16 [E][d_model][d_ff/32];  I8_ROW / FP8_ROW: fp32 [E][d_model];
  *                   E2M1: fp16 [E][d_ff/16][d_model] (scale of output o for neurons 16g..16g+15
- *                   at [g][o])
+ *                   at [g][o]);  MX4: uint8 [E][d_model][d_ff/32]
  *
  * Tiled layout (MOE_W_Q8_0_TILED, MOE_W_I8_ROW_TILED, MOE_W_FP8_ROW_TILED; made by
  * moe_repack_experts).  A matrix of
@@ -151,7 +165,7 @@ typedef struct {
 /* Size limits checked by every entry point (MOE_EINVAL beyond them):
  *   1 <= T <= 32768;  1 <= E <= 512;  1 <= k <= min(E, 64);
  *   d_model a multiple of 64, 64 <= d_model <= 16384;  d_ff a multiple of 32, 32 <= d_ff <= 16384,
- *   and a multiple of 64 for the int8 and fp8 formats (plain and tiled);  0 <= n_shared <= 4.
+ *   and a multiple of 64 for the int8 and fp8 formats (plain and tiled) and MX4;  0 <= n_shared <= 4.
  */
 
 /* Bytes of workspace the given call needs (0 if the arguments are invalid).  T, k, the expert
@@ -165,7 +179,9 @@ size_t moe_route_workspace_bytes(int32_t T, int32_t E);
  * Router only (step 1).  x [T][d_model] (xtype), w_router fp32 [E][d_model], router_bias fp32 [E]
  * or NULL.  Writes topk_idx int32 [T][k] in rank order (logit descending, ties to the lower
  * index) and topk_w fp32 [T][k] (renormalised, sums to 1).  Logits are accumulated in fp64, so
- * the selection is the exact-arithmetic one except for logits closer than ~1e-12 relative.
+ * the selection is the exact-arithmetic one except for logits closer than ~1e-12 relative.  They
+ * stay at the start of ws, fp64 [T][E], until something else uses it: what moe_balance_loss takes
+ * as MOE_X_F64.
  */
 moe_status moe_route(const void *x, int32_t xtype, int32_t T, int32_t d_model,
                      const float *w_router, const float *router_bias, int32_t E, int32_t k,
@@ -190,7 +206,8 @@ moe_status moe_permute(const int32_t *topk_idx, int32_t T, int32_t k, int32_t E,
  * fp32 [E] or NULL; out fp32 [T][d_model].  topk_idx_out / topk_w_out: optional ([T][k]) copies
  * of the routing, or NULL.
  * Supported: Q8_0 / I8_ROW with SwiGLU or ReLU^2; E2M1 with ReLU^2 (flags 0 or ZERO_SKIP) or
- * SwiGLU (flags 0); PREFILL_I8 with Q8_0 or I8_ROW + SwiGLU; PREFILL_FP8 with FP8_ROW + SwiGLU.
+ * SwiGLU (flags 0); PREFILL_I8 with Q8_0 or I8_ROW + SwiGLU; PREFILL_FP8 with FP8_ROW + SwiGLU;
+ * MX4 with SwiGLU or ReLU^2 (flags 0 or PREFILL_MX4).
  * Other combinations: MOE_EUNSUPPORTED.
  */
 moe_status moe_layer_forward(const void *x, int32_t xtype, int32_t T, const float *w_router,
@@ -259,6 +276,79 @@ moe_status moe_quantize_rows_fp8(const void *v, int32_t xtype, int32_t rows, int
                                  uint8_t *q, float *scale, void *stream);
 
 /*
+ * Quantises the rows of a [rows][cols] matrix v (xtype MOE_X_F32 or MOE_X_BF16) to MX4: per 32
+ * contiguous values, a = max|v|, e = floor(log2(a)) - 2 clamped to [-127, 127] (a = 0: -127), scale
+ * byte e + 127, codes = E2M1 of v * 2^-e by round to nearest, ties to the even code, saturating at
+ * 6 (the conversion of the OCP MX specification v1.0, section 6.3); the sign of a value that rounds
+ * to zero is kept.  A block that holds a NaN or an infinity gets the scale 0xFF and codes 0.
+ * q uint8 [rows][cols/2], scale uint8 [rows][cols/32].  values: NULL, or [rows][cols] of xtype, which
+ * receives what codes and scales stand for (exact in both types; NaN for a 0xFF block).  cols a
+ * multiple of 64, 64 <= cols <= 16384; 1 <= rows <= 2^24.
+ */
+moe_status moe_quantize_rows_mx4(const void *v, int32_t xtype, int32_t rows, int32_t cols, uint8_t *q,
+                                 uint8_t *scale, void *values, void *stream);
+
+/*
+ * Grouped product of rows with MX4 matrices, the experts' projections as an operator of its own:
+ *     out[r] = act(W[g] x[src(r)])   for the rows offsets[g] <= r < offsets[g + 1] of group g.
+ *   x       [x_rows][K] of xtype MOE_X_F32 or MOE_X_BF16 (each product exact, sums in fp32), or
+ *           MOE_X_MX4: codes uint8 [x_rows][K/2] with x_scales uint8 [x_rows][K/32] (x_scales is
+ *           NULL otherwise).
+ *   perm    int32 [rows] or NULL.  src(r) = perm[r] / k (moe_permute's pairs: the token of the
+ *           pair), clamped to [0, x_rows); without perm src(r) = r, k = 1 and x_rows >= rows.
+ *   w       uint8 [E][N][K/2] codes, w_scales uint8 [E][N][K/32] (as MOE_W_MX4).
+ *   offsets int32 [E+1], ascending, on the device (moe_permute's), or NULL with E = 1: all rows.
+ *           Values are clamped to [0, rows].  Rows that belong to no group are left as they were.
+ *   act     MOE_ACT_NONE: [rows][N];  MOE_ACT_RELU2: max(., 0)^2, [rows][N];  MOE_ACT_SWIGLU: gate
+ *           rows 0..N/2-1 of W, then up rows: silu(gate) * up, [rows][N/2] (N even).
+ *   out     [rows][N or N/2] of otype MOE_X_F32 or MOE_X_BF16 (rounded once, to nearest even), or
+ *           MOE_X_MX4 (x in MX4 only, out columns a multiple of 32): codes in out, scales in
+ *           out_scales uint8 [rows][columns/32], as moe_quantize_rows_mx4 on the fp32 result;
+ *           out_scales is NULL otherwise.
+ * K a multiple of 64, 64 <= K <= 16384; 1 <= N <= 65536; 1 <= E <= 512; 1 <= rows, x_rows <= 2^21;
+ * 1 <= k <= 64.  w_scales and x_scales hold 2 K/64 bytes a row.  An infinite fp32 value of x gives
+ * NaN in its row's outputs.  out and out_scales overlap none of the inputs.
+ */
+moe_status moe_matmul_mx4(const void *x, const uint8_t *x_scales, int32_t xtype, int32_t x_rows, int32_t K,
+                          const int32_t *perm, int32_t k, int32_t rows, const uint8_t *w, const uint8_t *w_scales,
+                          int32_t E, int32_t N, const int32_t *offsets, int32_t act, void *out,
+                          uint8_t *out_scales, int32_t otype, void *stream);
+
+/*
+ * The router's training losses over a batch, and its load counts.  logits [T][E] of ltype MOE_X_F32,
+ * MOE_X_BF16 or MOE_X_F64 (rounded to fp32 on reading; what moe_route leaves in its workspace);
+ * topk_idx int32 [T][k], ids clamped to [0, E) as moe_permute does, an id that a token names twice
+ * counts twice.  token_mask uint8 [T] or NULL: tokens with 0 are padding; a token whose logits are
+ * all -inf is taken as padding too.  What padding rows hold is not looked at.  Over the n tokens
+ * that remain, p_t = softmax(logits[t]) and lse_t = log sum exp:
+ *   counts    int32 [E]: pairs routed to each expert;  f_e = counts_e / (n k)
+ *   mean_prob fp32 [E]:  P_e = mean_t p_te
+ *   loss      fp32 [2]:  {E sum_e f_e P_e, mean_t lse_t^2}: the load-balancing loss (1 when even)
+ *                        and the z loss
+ * all zero for n = 0.  1 <= T <= 32768, 1 <= E <= 512, 1 <= k <= min(E, 64).  Sums run in fp32 in a
+ * fixed order.  ws: moe_balance_workspace_bytes(T, E), any contents.
+ */
+size_t moe_balance_workspace_bytes(int32_t T, int32_t E);
+moe_status moe_balance_loss(const void *logits, int32_t ltype, int32_t T, int32_t E, const int32_t *topk_idx,
+                            int32_t k, const uint8_t *token_mask, float *loss, int32_t *counts,
+                            float *mean_prob, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * The gradient with respect to the logits.  counts: moe_balance_loss's for the same batch (they
+ * carry n; for counts summed over several batches or GPUs, f and n are the sums').  d_loss fp32 [2]:
+ * the gradients of the two losses.  topk_w and d_topk_w fp32 [T][k], or both NULL: moe_route's
+ * renormalised weights and the gradient with respect to them.
+ *   d_logits[t][e] = p_te (d_loss[0] E/n (f_e - sum_j f_j p_tj) + d_loss[1] 2/n lse_t)
+ *                  + sum over the slots j with topk_idx[t][j] = e of w_tj (dw_tj - sum_i w_ti dw_ti)
+ * (f is a count: no gradient flows through it); zero rows for padding.  d_logits [T][E] of gtype
+ * MOE_X_F32 or MOE_X_BF16.
+ */
+moe_status moe_balance_loss_backward(const void *logits, int32_t ltype, int32_t T, int32_t E,
+                                     const int32_t *topk_idx, int32_t k, const uint8_t *token_mask,
+                                     const int32_t *counts, const float *d_loss, const float *topk_w,
+                                     const float *d_topk_w, void *d_logits, int32_t gtype, void *stream);
+
+/*
  * Diagnostics: the intermediate activations h (step 3's output, the down projection's input)
  * that the last moe_layer_forward (with_router = 1) or moe_experts_forward (with_router = 0)
  * call on workspace ws left there.  T, k, *ex, act and flags must be that call's; the stream must
@@ -270,6 +360,7 @@ moe_status moe_quantize_rows_fp8(const void *v, int32_t xtype, int32_t rows, int
  *   with MOE_F_PREFILL_I8 or MOE_F_PREFILL_FP8 only (otherwise both NULL, else MOE_EINVAL):
  *   hq [T k + S T][d_ff] the codes of h by rule Q (int8) or Q8 (E4M3 bytes), column order, and
  *   sh fp32 [T k + S T] their row scales.
+ * MOE_F_PREFILL_MX4 keeps no h: MOE_EUNSUPPORTED.
  * Not part of the layer's path: for checking the layer against a reference and for counting the
  * 16-neuron groups a zero-skip down projection reads.
  */

@@ -1,7 +1,7 @@
 """Seeded synthetic inputs for one sparse Mixture-of-Experts FFN layer.
 
 This module only draws random numbers and packs them into the byte formats the layer reads
-(Q8_0, per-row int8, E2M1 with an fp16 scale per 16 values, neuron-major down, per-row E4M3).  It holds none
+(Q8_0, per-row int8, E2M1 with an fp16 scale per 16 values, neuron-major down, per-row E4M3, MX4).  It holds none
 of the layer's arithmetic: no dequantisation, no matmul, no routing.  Both the HIP path and the
 CPU oracle consume the exact bytes produced here (the oracle gets a host copy).
 
@@ -36,10 +36,12 @@ import torch
 # Format / activation / x-type codes.  They mirror the enum values of the C ABI so the binding
 # can pass them through unchanged.
 FMT_Q8_0, FMT_I8_ROW, FMT_E2M1, FMT_FP8_ROW = 0, 1, 2, 5
+FMT_MX4 = 8
 ACT_SWIGLU, ACT_RELU2 = 0, 1
 X_F32, X_BF16 = 0, 1
 
-FMT_NAMES = {"q8_0": FMT_Q8_0, "i8_row": FMT_I8_ROW, "e2m1": FMT_E2M1, "fp8_row": FMT_FP8_ROW}
+FMT_NAMES = {"q8_0": FMT_Q8_0, "i8_row": FMT_I8_ROW, "e2m1": FMT_E2M1, "fp8_row": FMT_FP8_ROW,
+             "mx4": FMT_MX4}
 ACT_NAMES = {"swiglu": ACT_SWIGLU, "relu2": ACT_RELU2}
 
 # Per-tensor stream numbers.
@@ -189,6 +191,23 @@ def pack_e2m1_g16(w: torch.Tensor):
     return packed.contiguous(), s16, codes
 
 
+def pack_mx4(w: torch.Tensor):
+    """fp32 [..., N, K] -> (uint8 [..., N, K/2], uint8 E8M0 [..., N, K/32]): MXFP4.
+
+    Per 32 contiguous values along K: exponent e = floor(log2(max|w|)) - 2 (an all-zero block -127),
+    scale byte e + 127; code = nearest E2M1 value of w * 2^-e, saturating.  Two codes per byte,
+    element 2i in the low nibble.
+    """
+    *lead, N, K = w.shape
+    assert K % 32 == 0
+    b = w.reshape(*lead, N, K // 32, 32)
+    amax = b.abs().amax(dim=-1, keepdim=True)
+    e = torch.where(amax > 0, torch.frexp(amax).exponent - 3, -127).clamp(-127, 127)
+    codes = _e2m1_codes(torch.ldexp(b, -e)).reshape(*lead, N, K)
+    packed = codes[..., 0::2] | (codes[..., 1::2] << 4)
+    return packed.contiguous(), (e + 127).to(torch.uint8).reshape(*lead, N, K // 32)
+
+
 def neuron_major_down(codes: torch.Tensor, s16: torch.Tensor):
     """Re-lay an E2M1 down matrix out neuron-major (a pure byte permutation).
 
@@ -258,6 +277,11 @@ def make_layer(w: Workload, instance: int = 0, device="cpu", keep_codes: bool = 
         gus = torch.empty((NE, rows, d // 16), dtype=torch.float16, device=device)
         dn = torch.empty((NE, dff, d // 2), dtype=torch.uint8, device=device)
         dns = torch.empty((NE, dff // 16, d), dtype=torch.float16, device=device)
+    elif w.fmt == FMT_MX4:
+        gu = torch.empty((NE, rows, d // 2), dtype=torch.uint8, device=device)
+        gus = torch.empty((NE, rows, d // 32), dtype=torch.uint8, device=device)
+        dn = torch.empty((NE, d, dff // 2), dtype=torch.uint8, device=device)
+        dns = torch.empty((NE, d, dff // 32), dtype=torch.uint8, device=device)
     else:
         raise ValueError(w.fmt)
 
@@ -272,6 +296,8 @@ def make_layer(w: Workload, instance: int = 0, device="cpu", keep_codes: bool = 
             gu[e0:e1], gus[e0:e1] = pack_i8_row(wgu)
         elif w.fmt == FMT_FP8_ROW:
             gu[e0:e1], gus[e0:e1] = pack_fp8_row(wgu)
+        elif w.fmt == FMT_MX4:
+            gu[e0:e1], gus[e0:e1] = pack_mx4(wgu)
         else:
             gu[e0:e1], gus[e0:e1], _ = pack_e2m1_g16(wgu)
         del wgu
@@ -283,6 +309,8 @@ def make_layer(w: Workload, instance: int = 0, device="cpu", keep_codes: bool = 
             dn[e0:e1], dns[e0:e1] = pack_i8_row(wdn)
         elif w.fmt == FMT_FP8_ROW:
             dn[e0:e1], dns[e0:e1] = pack_fp8_row(wdn)
+        elif w.fmt == FMT_MX4:
+            dn[e0:e1], dns[e0:e1] = pack_mx4(wdn)
         else:
             _, s16, codes = pack_e2m1_g16(wdn)
             dn[e0:e1], dns[e0:e1] = neuron_major_down(codes, s16)
@@ -313,6 +341,8 @@ def expert_bytes(w: Workload) -> int:
         return rows * d + rows * (d // 32) * 2 + d * dff + d * (dff // 32) * 2
     if w.fmt in (FMT_I8_ROW, FMT_FP8_ROW):
         return rows * d + rows * 4 + d * dff + d * 4
+    if w.fmt == FMT_MX4:
+        return (rows + dff) * d // 2 + (rows + dff) * d // 32
     return rows * d // 2 + rows * (d // 16) * 2 + dff * d // 2 + (dff // 16) * d * 2
 
 

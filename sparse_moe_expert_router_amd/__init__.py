@@ -17,17 +17,19 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 # MOE_SANITIZE=1 loads the build whose host code carries AddressSanitizer / UBSan checks
 LIB_PATH = os.path.join(_PKG, "libmoe_san.so" if os.environ.get("MOE_SANITIZE") == "1" else "libmoe.so")
 
-X_F32, X_BF16 = 0, 1
+X_F32, X_BF16, X_MX4, X_F64 = 0, 1, 2, 3
 W_Q8_0, W_I8_ROW, W_E2M1_G16, W_Q8_0_TILED, W_I8_ROW_TILED = 0, 1, 2, 3, 4
 W_FP8_ROW, W_FP8_ROW_TILED = 5, 6
-ACT_SWIGLU, ACT_RELU2 = 0, 1
-F_ZERO_SKIP, F_PREFILL_I8, F_PREFILL_FP8 = 1, 4, 8
+W_MX4 = 8
+ACT_SWIGLU, ACT_RELU2, ACT_NONE = 0, 1, 2
+F_ZERO_SKIP, F_PREFILL_I8, F_PREFILL_FP8, F_PREFILL_MX4 = 1, 4, 8, 16
 OK, EINVAL, EUNSUPPORTED, EWORKSPACE, EHIP, ESCRATCH = 0, -1, -2, -3, -4, -5
 STATIC_WORKSPACE_BYTES = 64 << 20       # MOE_STATIC_WORKSPACE_BYTES: the buffer of layer_forward_static
 
 EXPORTED = ("moe_workspace_bytes", "moe_route_workspace_bytes", "moe_route", "moe_permute",
             "moe_layer_forward", "moe_layer_forward_static", "moe_experts_forward", "moe_quantize_rows_i8", "moe_quantize_rows_fp8",
-            "moe_repack_experts", "moe_read_intermediates",
+            "moe_repack_experts", "moe_read_intermediates", "moe_quantize_rows_mx4", "moe_matmul_mx4",
+            "moe_balance_workspace_bytes", "moe_balance_loss", "moe_balance_loss_backward",
             "moe_status_str", "moe_abi_version", "moe_profile_enable", "moe_profile_collect",
             "moe_profile_reset", "moe_profile_kinds", "moe_profile_get")
 
@@ -79,6 +81,16 @@ def lib():
         L.moe_quantize_rows_i8.restype = i32
         L.moe_quantize_rows_fp8.argtypes = [vp, i32, i32, i32, vp, vp, vp]
         L.moe_quantize_rows_fp8.restype = i32
+        L.moe_quantize_rows_mx4.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp]
+        L.moe_quantize_rows_mx4.restype = i32
+        L.moe_matmul_mx4.argtypes = [vp, vp, i32, i32, i32, vp, i32, i32, vp, vp, i32, i32, vp, i32, vp, vp, i32, vp]
+        L.moe_matmul_mx4.restype = i32
+        L.moe_balance_workspace_bytes.argtypes = [i32, i32]
+        L.moe_balance_workspace_bytes.restype = sz
+        L.moe_balance_loss.argtypes = [vp, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, sz, vp]
+        L.moe_balance_loss.restype = i32
+        L.moe_balance_loss_backward.argtypes = [vp, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, i32, vp]
+        L.moe_balance_loss_backward.restype = i32
         L.moe_read_intermediates.argtypes = [i32, i32, pex, i32, u32, i32, vp, sz, vp, vp, vp, vp]
         L.moe_read_intermediates.restype = i32
         L.moe_status_str.argtypes = [i32]
@@ -246,6 +258,178 @@ def quantize_rows_fp8(v):
     _check("moe_quantize_rows_fp8", lib().moe_quantize_rows_fp8(_p(v), _xtype(v), rows, cols, _p(q),
                                                                 _p(scale), _stream()))
     return q, scale
+
+
+# ---- MX4 operators and the router's training losses.  These check their tensors here (type, shape,
+# device, contiguity) and run on the current stream of the tensors' device.
+
+_XTYPES = {torch.float32: X_F32, torch.bfloat16: X_BF16, torch.float64: X_F64}
+
+
+def _need(name, t, dtypes, shape, dev):
+    """Raises unless t is a contiguous tensor on GPU `dev` of one of `dtypes` and of `shape` (None: any)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_cuda or t.device != dev:
+        raise ValueError(f"{name} must be on the GPU the call runs on ({dev}), got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _rows_of(name, t, dtypes):
+    """As _need, for the 2-d tensor that decides the call's device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+    _need(name, t, dtypes, None, t.device)
+    return t.device
+
+
+def _run(fn, dev, *args):
+    """Calls the library on `dev`'s current stream, with `dev` the current device."""
+    call = getattr(_lib or lib(), fn)
+    index = dev.index
+    if index == torch.cuda.current_device():
+        status = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != OK:
+        _check(fn, status)
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
+_LOGITS = (torch.float32, torch.bfloat16, torch.float64)
+_U8, _I32, _F32 = (torch.uint8,), (torch.int32,), (torch.float32,)
+_MASK = (torch.bool, torch.uint8)
+
+
+def quantize_rows_mx4(v, want_values: bool = False):
+    """moe_quantize_rows_mx4: (q uint8 [rows, cols/2], scale uint8 [rows, cols/32]) of v [rows, cols]
+    (float32 or bfloat16); with want_values also the values they stand for, in v's type."""
+    dev = _rows_of("v", v, _FLOATS)
+    rows, cols = v.shape
+    q = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
+    scale = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
+    values = torch.empty_like(v) if want_values else None
+    _run("moe_quantize_rows_mx4", dev, v.data_ptr(), _XTYPES[v.dtype], rows, cols, q.data_ptr(), scale.data_ptr(),
+         values.data_ptr() if want_values else None)
+    return (q, scale, values) if want_values else (q, scale)
+
+
+def matmul_mx4(x, w, w_scales, x_scales=None, offsets=None, perm=None, k: int = 1, act: int = ACT_NONE,
+               out_dtype=torch.bfloat16, out=None):
+    """moe_matmul_mx4: out[r] = act(W[g] x[perm[r] // k]) for the rows r of group g.
+
+    x [x_rows, K] float32 or bfloat16, or uint8 MX4 codes [x_rows, K/2] with x_scales; w uint8
+    [E, N, K/2] and w_scales uint8 [E, N, K/32] ([N, ..] for one group); offsets int32 [E+1] (None:
+    one group); perm int32 [rows] (None: row r reads x[r]).  out [rows, N] ([rows, N/2] with
+    ACT_SWIGLU) of out_dtype; rows outside every group are left as they were (unset in a new
+    tensor).  out_dtype uint8 (x in MX4 only) gives MX4 rows: a (codes, scales) pair."""
+    dev = _rows_of("x", x, (torch.float32, torch.bfloat16, torch.uint8))
+    mx = x.dtype == torch.uint8
+    x_rows, K = x.shape
+    if mx:
+        K *= 2
+        _need("x_scales", x_scales, _U8, (x_rows, K // 32), dev)
+    elif x_scales is not None:
+        raise ValueError("x_scales goes with x as MX4 codes only")
+    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
+        raise ValueError("w must be [E, N, K/2] or [N, K/2]")
+    lead = w.shape[:-1]
+    _need("w", w, _U8, (*lead, K // 2), dev)
+    _need("w_scales", w_scales, _U8, (*lead, K // 32), dev)
+    E, N = (lead[0], lead[1]) if len(lead) == 2 else (1, lead[0])
+    if offsets is not None:
+        _need("offsets", offsets, _I32, (E + 1,), dev)
+    elif E != 1:
+        raise ValueError("several groups need offsets")
+    if perm is not None:
+        _need("perm", perm, _I32, None, dev)
+        if perm.dim() != 1:
+            raise ValueError("perm must have one dimension")
+    rows = x_rows if perm is None else perm.shape[0]
+    cols = N // 2 if act == ACT_SWIGLU else N
+    scales = None
+    if out_dtype == torch.uint8:
+        if out is None:
+            out = (torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev),
+                   torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev))
+        codes, scales = out
+        _need("out[0]", codes, _U8, (rows, cols // 2), dev)
+        _need("out[1]", scales, _U8, (rows, cols // 32), dev)
+        otype, ptr, sptr = X_MX4, codes.data_ptr(), scales.data_ptr()
+    else:
+        if out_dtype not in _FLOATS:
+            raise TypeError(f"out_dtype must be float32, bfloat16 or uint8, got {out_dtype}")
+        if out is None:
+            out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+        else:
+            _need("out", out, (out_dtype,), (rows, cols), dev)
+        otype, ptr, sptr = _XTYPES[out_dtype], out.data_ptr(), None
+    _run("moe_matmul_mx4", dev, x.data_ptr(), x_scales.data_ptr() if mx else None, X_MX4 if mx else _XTYPES[x.dtype],
+         x_rows, K, None if perm is None else perm.data_ptr(), k, rows, w.data_ptr(), w_scales.data_ptr(), E, N,
+         None if offsets is None else offsets.data_ptr(), act, ptr, sptr, otype)
+    return out
+
+
+def _batch(logits, topk_idx, mask):
+    dev = _rows_of("logits", logits, _LOGITS)
+    T, E = logits.shape
+    _need("topk_idx", topk_idx, _I32, None, dev)
+    if topk_idx.dim() != 2 or topk_idx.shape[0] != T:
+        raise ValueError(f"topk_idx must have the shape ({T}, k), got {tuple(topk_idx.shape)}")
+    if mask is not None:
+        _need("mask", mask, _MASK, (T,), dev)
+    return dev, T, E, topk_idx.shape[1]
+
+
+def balance_loss(logits, topk_idx, mask=None, ws=None):
+    """moe_balance_loss: (loss fp32 [2] = balance loss and z loss, counts int32 [E], mean_prob fp32
+    [E]) of router logits [T, E] (float32, bfloat16 or float64) and the selected ids [T, k]; mask
+    [T] (bool or uint8): False for padding."""
+    dev, T, E, k = _batch(logits, topk_idx, mask)
+    L = _lib or lib()
+    if ws is None:
+        ws = torch.empty(max(int(L.moe_balance_workspace_bytes(T, E)), 256), dtype=torch.uint8, device=dev)
+    else:
+        _need("ws", ws, _U8, None, dev)
+    loss = torch.empty(2, dtype=torch.float32, device=dev)
+    counts = torch.empty(E, dtype=torch.int32, device=dev)
+    mean_prob = torch.empty(E, dtype=torch.float32, device=dev)
+    _run("moe_balance_loss", dev, logits.data_ptr(), _XTYPES[logits.dtype], T, E, topk_idx.data_ptr(), k,
+         None if mask is None else mask.data_ptr(), loss.data_ptr(), counts.data_ptr(), mean_prob.data_ptr(),
+         ws.data_ptr(), ws.numel())
+    return loss, counts, mean_prob
+
+
+def balance_loss_backward(logits, topk_idx, counts, d_loss, topk_w=None, d_topk_w=None, mask=None, grad_dtype=None):
+    """moe_balance_loss_backward: d_logits [T, E] for the gradients d_loss fp32 [2] of the two losses
+    and, with topk_w and d_topk_w fp32 [T, k], of the renormalised routing weights.  grad_dtype:
+    float32 or bfloat16 (None: the logits' type, float32 for float64 logits)."""
+    dev, T, E, k = _batch(logits, topk_idx, mask)
+    _need("counts", counts, _I32, (E,), dev)
+    _need("d_loss", d_loss, _F32, (2,), dev)
+    if (topk_w is None) != (d_topk_w is None):
+        raise ValueError("topk_w and d_topk_w go together")
+    if topk_w is not None:
+        _need("topk_w", topk_w, _F32, (T, k), dev)
+        _need("d_topk_w", d_topk_w, _F32, (T, k), dev)
+    if grad_dtype is None:
+        grad_dtype = torch.float32 if logits.dtype == torch.float64 else logits.dtype
+    if grad_dtype not in _FLOATS:
+        raise TypeError(f"grad_dtype must be float32 or bfloat16, got {grad_dtype}")
+    d_logits = torch.empty((T, E), dtype=grad_dtype, device=dev)
+    _run("moe_balance_loss_backward", dev, logits.data_ptr(), _XTYPES[logits.dtype], T, E, topk_idx.data_ptr(), k,
+         None if mask is None else mask.data_ptr(), counts.data_ptr(), d_loss.data_ptr(),
+         None if topk_w is None else topk_w.data_ptr(), None if topk_w is None else d_topk_w.data_ptr(),
+         d_logits.data_ptr(), _XTYPES[grad_dtype])
+    return d_logits
 
 
 def read_intermediates(T: int, k: int, experts: dict, act: int, flags: int, ws, with_router: bool = True):

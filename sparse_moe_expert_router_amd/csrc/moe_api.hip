@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "../../include/moe.h"
+#include "moe_common.hpp"
 #include "moe_launch.hpp"
 
 namespace moe {
@@ -23,6 +24,7 @@ namespace {
 using namespace moe;
 
 constexpr size_t ALIGN = 256;
+constexpr int MX_BLOCK_VALUES = 32;   // values that share one MX4 scale
 constexpr int MAX_T = 32768;
 constexpr int SMALL_T_SELECT = 64;    // top-k inside the single-workgroup permute up to this T
 
@@ -31,6 +33,9 @@ size_t up(size_t v) { return (v + ALIGN - 1) / ALIGN * ALIGN; }
 bool aligned16(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 constexpr uint32_t PREFILL_FLAGS = MOE_F_PREFILL_I8 | MOE_F_PREFILL_FP8;
+
+// Every flag that quantises the activations; PREFILL_FLAGS are those of the int8 / fp8 grouped GEMMs.
+constexpr uint32_t ALL_PREFILL_FLAGS = PREFILL_FLAGS | MOE_F_PREFILL_MX4;
 
 bool is_fp8(int fmt) { return fmt == MOE_W_FP8_ROW || fmt == MOE_W_FP8_ROW_TILED; }
 
@@ -71,6 +76,15 @@ Layout make_layout(int T, int k, int E, int S, int d, int d_ff, int fmt, uint32_
     L.tile_off = take(sizeof(int32_t) * (E + 1));
     L.scratch = take(sizeof(int32_t) * (size_t)permute_scratch_ints((int)P, E));
     L.tiles = take(sizeof(int4) * (size_t)prefill_tile_bound((int)PS, E + S));
+    if (flags & MOE_F_PREFILL_MX4) {             // codes and scales of x and h
+        L.xq = take((size_t)T * d / 2);
+        L.sx = take((size_t)T * d / MX_BLOCK_VALUES);
+        L.hq = take(PS * d_ff / 2);
+        L.sh = take(PS * d_ff / MX_BLOCK_VALUES);
+        L.ybuf = take(sizeof(float) * PS * d);
+        L.total = o;
+        return L;
+    }
     L.h = take(sizeof(float) * PS * d_ff);    // fp32 h, or the two bf16 planes of h
     if (fmt == MOE_W_E2M1_G16) {
         L.ybuf = take(sizeof(float) * PS * (size_t)e2m1_down_chunks(d_ff, T) * d);
@@ -91,18 +105,21 @@ Layout make_layout(int T, int k, int E, int S, int d, int d_ff, int fmt, uint32_
 moe_status check_experts(const moe_experts *ex, int act, uint32_t flags)
 {
     if (!ex) return MOE_EINVAL;
-    if (ex->fmt < MOE_W_Q8_0 || ex->fmt > MOE_W_FP8_ROW_TILED) return MOE_EINVAL;
+    if ((ex->fmt < MOE_W_Q8_0 || ex->fmt > MOE_W_FP8_ROW_TILED) && ex->fmt != MOE_W_MX4) return MOE_EINVAL;
     if (act != MOE_ACT_SWIGLU && act != MOE_ACT_RELU2) return MOE_EINVAL;
     if (ex->E < 1 || ex->E > MAX_E) return MOE_EINVAL;
     if (ex->n_shared < 0 || ex->n_shared > MAX_SHARED) return MOE_EINVAL;
     if (ex->d_model < 64 || ex->d_model > 16384 || ex->d_model % 64) return MOE_EINVAL;
     if (ex->d_ff < 32 || ex->d_ff > 16384 || ex->d_ff % 32) return MOE_EINVAL;
     if (ex->fmt != MOE_W_E2M1_G16 && ex->d_ff % 64) return MOE_EINVAL;
-    if (flags & ~(uint32_t)(MOE_F_ZERO_SKIP | PREFILL_FLAGS)) return MOE_EINVAL;
-    if ((flags & PREFILL_FLAGS) == PREFILL_FLAGS) return MOE_EINVAL;
+    if (flags & ~(uint32_t)(MOE_F_ZERO_SKIP | ALL_PREFILL_FLAGS)) return MOE_EINVAL;
+    const uint32_t pf = flags & ALL_PREFILL_FLAGS;
+    if (pf & (pf - 1)) return MOE_EINVAL;             // one prefill definition at a time
     if ((flags & MOE_F_ZERO_SKIP) && ex->fmt != MOE_W_E2M1_G16) return MOE_EUNSUPPORTED;
     if ((flags & MOE_F_PREFILL_I8) && (ex->fmt == MOE_W_E2M1_G16 || is_fp8(ex->fmt) || act != MOE_ACT_SWIGLU))
         return MOE_EUNSUPPORTED;
+    if ((flags & MOE_F_PREFILL_MX4) && ex->fmt != MOE_W_MX4) return MOE_EUNSUPPORTED;
+    if ((flags & PREFILL_FLAGS) && ex->fmt == MOE_W_MX4) return MOE_EUNSUPPORTED;
     // E4M3 experts run on the fp8 prefill path only, and that path on them only
     if (is_fp8(ex->fmt) != ((flags & MOE_F_PREFILL_FP8) != 0)) return MOE_EUNSUPPORTED;
     if ((flags & MOE_F_PREFILL_FP8) && act != MOE_ACT_SWIGLU) return MOE_EUNSUPPORTED;
@@ -142,6 +159,65 @@ PermuteOut permute_view(void *ws, const Layout &L)
                       at<int32_t>(ws, L.tile_off), at<int32_t>(ws, L.scratch), at<int4>(ws, L.tiles)};
 }
 
+// Steps 3-5 of MX4 experts: two grouped products and the combine.  With MOE_F_PREFILL_MX4 the gate/up
+// product's epilogue writes h as MX4 rows, which the down product takes as they are.
+moe_status run_experts_mx4(const void *x, int xtype, int T, int k, const moe_experts *ex, int act, uint32_t flags,
+                           const float *topk_w, float *out, void *ws, const Layout &L, const PermuteOut &po,
+                           hipStream_t s)
+{
+    const int P = T * k, PS = P + ex->n_shared * T, d = ex->d_model;
+    const bool quant = (flags & MOE_F_PREFILL_MX4) != 0;
+    float *ybuf = at<float>(ws, L.ybuf);
+    Mx4Product p{};
+    p.E = ex->E;
+    p.S = ex->n_shared;
+    p.T = T;
+    p.Pr = P;
+    p.offsets = po.offsets;
+    // gate/up, rows gathered from the tokens
+    p.rows_x = T;
+    p.K = d;
+    p.perm = po.perm;
+    p.k = k;
+    p.w = static_cast<const uint8_t *>(ex->gate_up);
+    p.ws = static_cast<const uint8_t *>(ex->gate_up_scales);
+    p.N = (act == MOE_ACT_SWIGLU ? 2 : 1) * ex->d_ff;
+    p.act = act;
+    if (quant) {
+        uint8_t *xq = at<uint8_t>(ws, L.xq), *sx = at<uint8_t>(ws, L.sx);
+        if (launch_quantize_mx4(x, xtype, T, d, xq, sx, nullptr, s) != hipSuccess) return MOE_EHIP;
+        p.x = xq;
+        p.xs = sx;
+        p.xtype = X_MX4;
+        p.out = at<uint8_t>(ws, L.hq);
+        p.out_scales = at<uint8_t>(ws, L.sh);
+        p.otype = X_MX4;
+    } else {
+        p.x = x;
+        p.xtype = xtype;
+        p.out = at<float>(ws, L.h);
+        p.otype = X_F32;
+    }
+    if (launch_product_mx4(p, s) != hipSuccess) return MOE_EHIP;
+    // down, rows as they lie
+    p.x = p.out;
+    p.xs = p.out_scales;
+    p.xtype = p.otype;
+    p.rows_x = PS;
+    p.K = ex->d_ff;
+    p.perm = nullptr;
+    p.k = 1;
+    p.w = static_cast<const uint8_t *>(ex->down);
+    p.ws = static_cast<const uint8_t *>(ex->down_scales);
+    p.N = d;
+    p.act = MOE_ACT_NONE;
+    p.out = ybuf;
+    p.out_scales = nullptr;
+    p.otype = X_F32;
+    if (launch_product_mx4(p, s) != hipSuccess) return MOE_EHIP;
+    return from_hip(launch_combine_rows(ybuf, po.inv, topk_w, T, k, d, 1, ex->n_shared, out, s));
+}
+
 // Steps 3-5 once the permutation is in the workspace.
 moe_status run_experts(const void *x, int xtype, int T, int k, const moe_experts *ex, int act,
                        uint32_t flags, const int32_t *topk_idx, const float *topk_w, float *out, void *ws,
@@ -150,6 +226,7 @@ moe_status run_experts(const void *x, int xtype, int T, int k, const moe_experts
 {
     const ExpertsDev dv = dev_view(ex);
     const PermuteOut po = permute_view(ws, L);
+    if (ex->fmt == MOE_W_MX4) return run_experts_mx4(x, xtype, T, k, ex, act, flags, topk_w, out, ws, L, po, s);
     float *h = at<float>(ws, L.h);
     hipError_t err;
     if (flags & PREFILL_FLAGS) {
@@ -328,8 +405,9 @@ moe_status moe_layer_forward(const void *x, int32_t xtype, int32_t T, const floa
                                           logits, s);
     if (err != hipSuccess) return MOE_EHIP;
     const int BM = (flags & PREFILL_FLAGS) ? prefill_tile_rows() : 0;
-    const bool route_in_experts = ex->fmt == MOE_W_E2M1_G16 ? up_e2m1_can_route(T, k, ex->E, ex->d_model)
-                                                            : gateup_can_route(T, k, ex->E);
+    const bool route_in_experts = ex->fmt == MOE_W_MX4        ? false
+                                  : ex->fmt == MOE_W_E2M1_G16 ? up_e2m1_can_route(T, k, ex->E, ex->d_model)
+                                                              : gateup_can_route(T, k, ex->E);
     if (!(flags & PREFILL_FLAGS) && route_in_experts)
         return run_experts(x, xtype, T, k, ex, act, flags, idx, w, out, ws, L, s, logits, idx, w);
     if (T <= SMALL_T_SELECT) {
@@ -395,6 +473,7 @@ moe_status moe_read_intermediates(int32_t T, int32_t k, const moe_experts *ex, i
     if (st != MOE_OK) return st;
     if (check_tk(T, k, ex->E) != MOE_OK) return MOE_EINVAL;
     if (!aligned16(ws) || !aligned16(h)) return MOE_EINVAL;
+    if (flags & MOE_F_PREFILL_MX4) return MOE_EUNSUPPORTED;
     const bool prefill = (flags & PREFILL_FLAGS) != 0;
     if (prefill != (hq != nullptr) || prefill != (sh != nullptr)) return MOE_EINVAL;
     if (prefill && (!aligned16(hq) || !aligned16(sh))) return MOE_EINVAL;
@@ -406,7 +485,7 @@ moe_status moe_read_intermediates(int32_t T, int32_t k, const moe_experts *ex, i
     const int P = T * k, rows = P + ex->n_shared * T;
     const float *h32 = nullptr;
     const uint16_t *hh = nullptr, *hl = nullptr;
-    if (prefill || ex->fmt == MOE_W_E2M1_G16) {
+    if (prefill || ex->fmt == MOE_W_E2M1_G16 || ex->fmt == MOE_W_MX4) {
         h32 = at<float>(w, L.h);
     } else {                                          // int8 decode: two bf16 planes
         hh = at<uint16_t>(w, L.h);
@@ -478,6 +557,96 @@ moe_status moe_quantize_rows_fp8(const void *v, int32_t xtype, int32_t rows, int
     if (!aligned16(v) || !aligned16(q) || !aligned16(scale)) return MOE_EINVAL;
     return from_hip(launch_quantize_rows(v, xtype, rows, cols, reinterpret_cast<int8_t *>(q), scale, false, true,
                                          static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_quantize_rows_mx4(const void *v, int32_t xtype, int32_t rows, int32_t cols, uint8_t *q,
+                                 uint8_t *scale, void *values, void *stream)
+{
+    if (xtype != MOE_X_F32 && xtype != MOE_X_BF16) return MOE_EINVAL;
+    if (rows < 1 || rows > (1 << 24) || cols < 64 || cols > 16384 || cols % 64) return MOE_EINVAL;
+    if (!aligned16(v) || !aligned16(q) || !aligned16(scale)) return MOE_EINVAL;
+    if (values && !aligned16(values)) return MOE_EINVAL;
+    return from_hip(launch_quantize_mx4(v, xtype, rows, cols, q, scale, values, static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_matmul_mx4(const void *x, const uint8_t *x_scales, int32_t xtype, int32_t x_rows, int32_t K,
+                          const int32_t *perm, int32_t k, int32_t rows, const uint8_t *w, const uint8_t *w_scales,
+                          int32_t E, int32_t N, const int32_t *offsets, int32_t act, void *out,
+                          uint8_t *out_scales, int32_t otype, void *stream)
+{
+    constexpr int32_t MAX_ROWS = 1 << 21;
+    if (xtype != MOE_X_F32 && xtype != MOE_X_BF16 && xtype != MOE_X_MX4) return MOE_EINVAL;
+    if (otype != MOE_X_F32 && otype != MOE_X_BF16 && otype != MOE_X_MX4) return MOE_EINVAL;
+    if (act != MOE_ACT_SWIGLU && act != MOE_ACT_RELU2 && act != MOE_ACT_NONE) return MOE_EINVAL;
+    if (rows < 1 || rows > MAX_ROWS || x_rows < 1 || x_rows > MAX_ROWS || k < 1 || k > MAX_K) return MOE_EINVAL;
+    if (K < 64 || K > 16384 || K % 64 || N < 1 || N > 65536 || E < 1 || E > MAX_E) return MOE_EINVAL;
+    if (act == MOE_ACT_SWIGLU && N % 2) return MOE_EINVAL;
+    if (!perm && (k != 1 || x_rows < rows)) return MOE_EINVAL;
+    if (!offsets && E != 1) return MOE_EINVAL;
+    if (!aligned16(x) || !aligned16(w) || !aligned16(w_scales) || !aligned16(out)) return MOE_EINVAL;
+    if ((perm && !aligned16(perm)) || (offsets && !aligned16(offsets))) return MOE_EINVAL;
+    if (xtype == MOE_X_MX4 ? !aligned16(x_scales) : x_scales != nullptr) return MOE_EINVAL;
+    if (otype == MOE_X_MX4 ? !aligned16(out_scales) : out_scales != nullptr) return MOE_EINVAL;
+    const int columns = act == MOE_ACT_SWIGLU ? N / 2 : N;
+    if (otype == MOE_X_MX4 && (xtype != MOE_X_MX4 || columns % MX_BLOCK_VALUES)) return MOE_EUNSUPPORTED;
+    Mx4Product p{};
+    p.x = x;
+    p.xs = x_scales;
+    p.xtype = xtype;
+    p.rows_x = x_rows;
+    p.K = K;
+    p.perm = perm;
+    p.k = k;
+    p.Pr = rows;
+    p.w = w;
+    p.ws = w_scales;
+    p.E = E;
+    p.N = N;
+    p.offsets = offsets;
+    p.act = act;
+    p.otype = otype;
+    p.out = out;
+    p.out_scales = out_scales;
+    return from_hip(launch_product_mx4(p, static_cast<hipStream_t>(stream)));
+}
+
+size_t moe_balance_workspace_bytes(int32_t T, int32_t E)
+{
+    if (T < 1 || T > MAX_T || E < 1 || E > MAX_E) return 0;
+    return balance_workspace_bytes(T, E);
+}
+
+moe_status moe_balance_loss(const void *logits, int32_t ltype, int32_t T, int32_t E, const int32_t *topk_idx,
+                            int32_t k, const uint8_t *token_mask, float *loss, int32_t *counts,
+                            float *mean_prob, void *ws, size_t ws_bytes, void *stream)
+{
+    if (ltype != MOE_X_F32 && ltype != MOE_X_BF16 && ltype != MOE_X_F64) return MOE_EINVAL;
+    if (E < 1 || E > MAX_E || check_tk(T, k, E) != MOE_OK) return MOE_EINVAL;
+    if (!aligned16(logits) || !aligned16(topk_idx) || !aligned16(loss) || !aligned16(counts) ||
+        !aligned16(mean_prob) || !aligned16(ws))
+        return MOE_EINVAL;
+    if (token_mask && !aligned16(token_mask)) return MOE_EINVAL;
+    if (ws_bytes < moe_balance_workspace_bytes(T, E)) return MOE_EWORKSPACE;
+    return from_hip(launch_balance_loss(logits, ltype, T, E, topk_idx, k, token_mask, loss, counts, mean_prob, ws,
+                                        static_cast<hipStream_t>(stream)));
+}
+
+moe_status moe_balance_loss_backward(const void *logits, int32_t ltype, int32_t T, int32_t E,
+                                     const int32_t *topk_idx, int32_t k, const uint8_t *token_mask,
+                                     const int32_t *counts, const float *d_loss, const float *topk_w,
+                                     const float *d_topk_w, void *d_logits, int32_t gtype, void *stream)
+{
+    if (ltype != MOE_X_F32 && ltype != MOE_X_BF16 && ltype != MOE_X_F64) return MOE_EINVAL;
+    if (gtype != MOE_X_F32 && gtype != MOE_X_BF16) return MOE_EINVAL;
+    if (E < 1 || E > MAX_E || check_tk(T, k, E) != MOE_OK) return MOE_EINVAL;
+    if (!aligned16(logits) || !aligned16(topk_idx) || !aligned16(counts) || !aligned16(d_loss) ||
+        !aligned16(d_logits))
+        return MOE_EINVAL;
+    if (token_mask && !aligned16(token_mask)) return MOE_EINVAL;
+    if ((topk_w == nullptr) != (d_topk_w == nullptr)) return MOE_EINVAL;
+    if (topk_w && (!aligned16(topk_w) || !aligned16(d_topk_w))) return MOE_EINVAL;
+    return from_hip(launch_balance_grad(logits, ltype, T, E, topk_idx, k, token_mask, counts, d_loss, topk_w,
+                                        d_topk_w, d_logits, gtype, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -15,7 +15,7 @@ constexpr int MAX_SHARED = 4;    // shared experts per layer
 // Kernel kinds for the opt-in HIP-event timer (names in prof.hip).
 enum KernelKind {
     K_ROUTER = 0, K_TOPK, K_PERMUTE, K_GATEUP_I8, K_DOWN_I8, K_COMBINE, K_UP_E2M1, K_DOWN_E2M1,
-    K_QUANT, K_GG_GATEUP, K_GG_DOWN, K_COUNT
+    K_QUANT, K_GG_GATEUP, K_GG_DOWN, K_PRODUCT_MX4, K_BALANCE, K_COUNT
 };
 
 // Brackets one kernel launch with HIP events on its stream while timing is enabled.
@@ -135,6 +135,36 @@ hipError_t launch_ggemm_gateup_i8(const int8_t *xq, const float *sx, int T, int 
                                   const PermuteOut &po, float *h, hipStream_t s);
 hipError_t launch_ggemm_down_i8(const int8_t *hq, const float *sh, int T, int k, const ExpertsDev &ex,
                                 const PermuteOut &po, float *ybuf, hipStream_t s);
+
+// MX4 (mx4.hip).  values != nullptr: also the rounded values in v's type.
+hipError_t launch_quantize_mx4(const void *v, int xtype, int rows, int cols, uint8_t *q, uint8_t *scale, void *values,
+                               hipStream_t s);
+
+// out[r] = act(W[g(r)] x[src(r)]) over rows grouped by `offsets` (see moe_matmul_mx4).  S shared
+// groups of T rows each follow the E groups: group E + s holds rows Pr + s T .. Pr + (s + 1) T - 1.
+struct Mx4Product {
+    const void *x;              // xtype X_F32, X_BF16 or X_MX4 rows of K values
+    const uint8_t *xs;          // X_MX4: E8M0 scales [rows_x][K / 32]
+    int xtype, rows_x, K;
+    const int32_t *perm;        // row r reads x[perm[r] / k], or x[r] (nullptr)
+    int k, Pr;                  // Pr grouped rows
+    const uint8_t *w, *ws;      // [E + S][N][K / 2] codes, [E + S][N][K / 32] scales
+    int E, N, S, T;
+    const int32_t *offsets;     // [E + 1], or nullptr: one group of Pr rows
+    int act, otype;             // otype X_F32, X_BF16 or X_MX4
+    void *out;
+    uint8_t *out_scales;        // X_MX4
+};
+hipError_t launch_product_mx4(const Mx4Product &p, hipStream_t s);
+
+// Router balance loss (balance.hip)
+size_t balance_workspace_bytes(int T, int E);
+hipError_t launch_balance_loss(const void *logits, int ltype, int T, int E, const int32_t *idx, int k,
+                               const uint8_t *mask, float *loss, int32_t *counts, float *mean_prob, void *ws,
+                               hipStream_t s);
+hipError_t launch_balance_grad(const void *logits, int ltype, int T, int E, const int32_t *idx, int k,
+                               const uint8_t *mask, const int32_t *counts, const float *d_loss, const float *topk_w,
+                               const float *d_topk_w, void *d_logits, int gtype, hipStream_t s);
 
 // Diagnostics (diag.hip): the workspace's intermediate activations in pair order.
 // h32 != nullptr: fp32 h rows; otherwise the sum of the two bf16 planes.

@@ -14,7 +14,8 @@ namespace {
 
 const char *const KERNEL_NAMES[K_COUNT] = {
     "router_logits", "topk", "select_permute", "gateup_int8", "down_int8", "combine_rows",
-    "up_e2m1", "down_e2m1", "quantize_rows", "ggemm_gateup_i8", "ggemm_down_i8"};
+    "up_e2m1", "down_e2m1", "quantize_rows", "ggemm_gateup_i8", "ggemm_down_i8",
+    "product_mx4", "balance"};
 
 struct Pending {
     int kind;
