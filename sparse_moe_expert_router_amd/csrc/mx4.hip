@@ -9,6 +9,7 @@
 //    rows per group, where streaming the weights is all that counts.
 #include <hip/hip_runtime.h>
 
+#include <cstdlib>
 #include "moe_launch.hpp"
 #include "mx4_dev.hpp"
 
@@ -129,6 +130,51 @@ __device__ __forceinline__ Tile find_tile(const Mx4Product &p, int tile, int bm,
     return Tile{0, 0, 0};
 }
 
+// The `slot`-th group that holds rows, all of its rows.  A group holds rows or not, so a ballot and
+// bit counts find it; the loads of all groups' offsets go out together.
+__device__ __forceinline__ Tile find_slot(const Mx4Product &p, int slot, int lane)
+{
+    if (p.offsets == nullptr) return Tile{0, 0, slot == 0 ? p.Pr : 0};
+    const int G = p.E + p.S;
+    constexpr int NC = (MAX_E + MAX_SHARED + 63) / 64;
+    int lo[NC], hi[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int g = 64 * c + lane;
+        lo[c] = hi[c] = 0;
+        if (64 * c < G) {
+            if (g < p.E) {
+                lo[c] = p.offsets[g];
+                hi[c] = p.offsets[g + 1];
+            } else if (g < G) {
+                lo[c] = p.Pr + (g - p.E) * p.T;
+                hi[c] = lo[c] + p.T;
+            }
+        }
+    }
+    Tile t{0, 0, 0};
+    int before = 0;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        if (64 * c < G) {
+            if (64 * c + lane < p.E) {
+                lo[c] = min(max(lo[c], 0), p.Pr);
+                hi[c] = min(max(hi[c], lo[c]), p.Pr);
+            }
+            const unsigned long long m = __ballot(hi[c] > lo[c]);
+            const int n = __popcll(m);
+            if (slot >= before && slot < before + n) {
+                const unsigned long long below = (1ull << lane) - 1;
+                const unsigned long long at = __ballot(((m >> lane) & 1) && __popcll(m & below) == slot - before);
+                const int l = __ffsll((long long)at) - 1;
+                t = Tile{64 * c + l, __shfl(lo[c], l, WAVE), __shfl(hi[c], l, WAVE) - __shfl(lo[c], l, WAVE)};
+            }
+            before += n;
+        }
+    }
+    return t;
+}
+
 __device__ __forceinline__ int source_row(const Mx4Product &p, int r)
 {
     if (p.perm == nullptr) return min(r, p.rows_x - 1);
@@ -173,9 +219,14 @@ __device__ __forceinline__ void store4(const Mx4Product &p, int row, int n0, int
 // Product of MX4 rows.  A block of 4 waves computes BM = 128 rows by BN = 256 weight rows (128 gate
 // rows and their 128 up rows with SwiGLU); wave w owns 64 of the weight rows and all 128 rows.
 // Weights are the A operand (their rows become 4 consecutive outputs of a lane), x the B operand.
-// Weights go from global memory into registers (no other wave wants them); x goes through LDS.
+// An MFMA lane holds one row's 16 bytes, so neighbouring lanes hold different rows: loaded straight
+// into registers, every lane would be a cache access of its own (64 per KB).  Both operands
+// therefore go through LDS by direct-to-LDS loads whose neighbouring lanes read neighbouring bytes
+// (16 accesses per KB), double-buffered in stages of 128 columns.
 
-constexpr int PB_M = 128, PB_N = 256, PB_KS = 256;     // rows, weight rows, K of an LDS stage
+constexpr int PB_M = 128, PB_N = 256;                  // rows, weight rows of a block
+constexpr int PB_X = PB_M * 64, PB_W = PB_N * 64;      // bytes of a stage's codes (128 columns)
+constexpr int PB_STAGE = PB_X + PB_W + 4 * (PB_M + PB_N);   // and 4 scale bytes per row
 
 __device__ __forceinline__ void lds_dma16(const void *g, uint32_t lds)
 {
@@ -188,16 +239,27 @@ __device__ __forceinline__ uint32_t lds_addr(T *p)
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void *)p;
 }
 
+// Orders LDS between the waves of a block; unlike __syncthreads() it leaves global loads in flight.
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 __device__ __forceinline__ i32x8v code_reg(const uint4 &v)
 {
     return i32x8v{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0};
 }
 
-// One K step's weights of a wave: 4 fragments of 16 rows by 128 columns.
-struct WStep {
-    uint4 c[4];
-    uint32_t s[4];       // this lane's scale code in the low byte
-};
+// Where a stage keeps 16-byte chunk c of row r (64-byte rows): the 16 rows that the 16 lanes of a
+// fragment read at once fall on different banks.
+__device__ __forceinline__ int chunk_at(int r, int c) { return r * 64 + 16 * (c ^ ((r >> 2) & 3)); }
+
+// The four scale bytes of columns 128 s .. of a row (`row`: its scales), 1 for the missing ones.
+// Rows of scales start at even addresses only.
+__device__ __forceinline__ uint32_t scales4(const uint8_t *row, int s, bool half)
+{
+    uint32_t v;
+    if (half) return *reinterpret_cast<const uint16_t *>(row + 4 * s) | 0x7F7F0000u;
+    __builtin_memcpy(&v, __builtin_assume_aligned(row + 4 * s, 2), 4);
+    return v;
+}
 
 // MG: 32-row groups of the tile that hold rows.
 template <int MG>
@@ -208,81 +270,47 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
     const bool glu = p.act == ACT_SWIGLU;
     const int F = p.N >> 1, NO = glu ? F : p.N;
     const int KB = p.K >> 1, KSC = p.K >> 5;              // bytes of codes, of scales per row
-    const int steps = (p.K + 127) >> 7, stages = (p.K + PB_KS - 1) / PB_KS;
+    const int steps = (p.K + 127) >> 7;
     const bool half = (p.K & 127) != 0;                   // the last step holds 64 columns
-    uint8_t *xsc = lds + 2 * PB_M * (PB_KS / 2);          // x scales: [step][lane][fragment]
 
-    // ---- x scales of the tile, transposed so that a lane reads all fragments' in one go
-    for (int i = tid; i < 16 * (KSC >> 1); i += 256) {
-        const int r = i & 15, pr = i >> 4;                // row within a fragment, pair of blocks
-        uint32_t b[8];
-#pragma unroll
-        for (int f = 0; f < 8; ++f) {
-            b[f] = 0;
-            if (f < MF) {
-                const int row = min(16 * f + r, t.rows - 1);
-                b[f] = *reinterpret_cast<const uint16_t *>(p.xs + (size_t)source_row(p, t.row0 + row) * KSC + 2 * pr);
-            }
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t w[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                w[j] = 0;
-#pragma unroll
-                for (int f = 0; f < 4; ++f) w[j] |= ((b[4 * j + f] >> (8 * h)) & 0xFFu) << (8 * f);
-            }
-            const int kb = 2 * pr + h;                    // = 4 step + lane group
-            *reinterpret_cast<uint2 *>(xsc + (size_t)(kb >> 2) * 512 + (kb & 3) * 128 + r * 8) = make_uint2(w[0], w[1]);
-        }
-    }
-    if (half && tid < 32)                                 // the missing blocks' scales: 1
-        *reinterpret_cast<uint2 *>(xsc + (size_t)(steps - 1) * 512 + 256 + tid * 8) = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
-
-    // ---- x codes: an LDS stage holds 128 bytes of every row, chunk c of row r at c ^ ((r >> 1) & 7)
-    const uint8_t *xp[MG];
-    int xc[MG];
-#pragma unroll
-    for (int i = 0; i < MG; ++i) {
-        const int slot = (i * 4 + wave) * 64 + lane, r = slot >> 3;
-        xp[i] = static_cast<const uint8_t *>(p.x) + (size_t)source_row(p, t.row0 + min(r, t.rows - 1)) * KB;
-        xc[i] = 16 * ((slot & 7) ^ ((r >> 1) & 7));
-    }
-    auto issue = [&](int st) {
-        const uint32_t L = lds_addr(lds + (st & 1) * PB_M * (PB_KS / 2));
-#pragma unroll
-        for (int i = 0; i < MG; ++i)
-            lds_dma16(xp[i] + min(st * (PB_KS / 2) + xc[i], KB - 16), L + (i * 4 + wave) * 1024);
+    // weight row that row r of the block's 256 stands for: wave w's 64 rows are 32 gate and their 32
+    // up rows with SwiGLU
+    auto weight_row = [&](int r) {
+        int n = nt * 256 + r;
+        if (glu) n = min(nt * 128 + (r >> 6) * 32 + (r & 31), F - 1) + ((r & 32) ? F : 0);
+        return (size_t)t.g * p.N + min(n, p.N - 1);
     };
-
-    // ---- weights
-    const uint8_t *wp[4], *sp[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        int n;
-        if (glu) {
-            const int f = min(nt * 128 + wave * 32 + 16 * (j & 1) + li, F - 1);
-            n = j < 2 ? f : F + f;
-        } else {
-            n = min(nt * 256 + wave * 64 + 16 * j + li, p.N - 1);
-        }
-        const size_t row = (size_t)t.g * p.N + n;
-        wp[j] = p.w + row * KB + 16 * lg;
-        sp[j] = p.ws + row * KSC + lg;
-    }
     const bool live = (glu ? nt * 128 + wave * 32 : nt * 256 + wave * 64) < NO;
-    auto wload = [&](WStep &w, int s) {
-        const bool in = live && s < steps && !(half && s == steps - 1 && lg >= 2);
+
+    // ---- sources: 4 lanes read a row's 64 bytes; instruction i of a wave fills 16 rows
+    constexpr int XI = (MF + 3) / 4;                      // x instructions of a wave
+    const uint8_t *wsrc[4], *xsrc[XI];
+    const int drow = lane >> 2, dchunk = 16 * ((lane & 3) ^ ((lane >> 4) & 3));   // (row >> 2) & 3 of row = lane / 4
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            w.c[j] = make_uint4(0, 0, 0, 0);
-            w.s[j] = 127;
-            if (in) {
-                w.c[j] = *reinterpret_cast<const uint4 *>(wp[j] + (size_t)s * 64);
-                w.s[j] = sp[j][s * 4];
-            }
+    for (int i = 0; i < 4; ++i) wsrc[i] = p.w + weight_row(64 * wave + 16 * i + drow) * KB;
+#pragma unroll
+    for (int i = 0; i < XI; ++i) {
+        const int r = 16 * (wave + 4 * i) + drow;
+        xsrc[i] = static_cast<const uint8_t *>(p.x) + (size_t)source_row(p, t.row0 + min(r, t.rows - 1)) * KB;
+    }
+    const uint8_t *wsc = p.ws + weight_row(tid) * KSC;    // thread r: scales of weight row r, of row r
+    const uint8_t *xsc = p.xs + (size_t)source_row(p, t.row0 + min(tid & (PB_M - 1), t.rows - 1)) * KSC;
+
+    auto issue = [&](int s) {
+        const uint32_t L = lds_addr(lds + (s & 1) * PB_STAGE);
+        const int off = min(s * 64 + dchunk, KB - 16);
+#pragma unroll
+        for (int i = 0; i < XI; ++i)
+            if (wave + 4 * i < MF) lds_dma16(xsrc[i] + off, L + (wave + 4 * i) * 1024);
+        if (live) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lds_dma16(wsrc[i] + off, L + PB_X + (4 * wave + i) * 1024);
         }
+    };
+    auto put_scales = [&](int s, uint32_t w, uint32_t x) {
+        uint8_t *S = lds + (s & 1) * PB_STAGE + PB_X + PB_W;
+        reinterpret_cast<uint32_t *>(S)[tid] = w;
+        if (tid < PB_M) reinterpret_cast<uint32_t *>(S + 4 * PB_N)[tid] = x;
     };
 
     f32x4 acc[4][MF];
@@ -291,40 +319,41 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
 #pragma unroll
         for (int f = 0; f < MF; ++f) acc[j][f] = zero4();
 
-    auto step = [&](const WStep &w, int s) {
-        const uint8_t *L = lds + ((s >> 1) & 1) * PB_M * (PB_KS / 2);
-        const uint2 xs = *reinterpret_cast<const uint2 *>(xsc + (size_t)s * 512 + lane * 8);
+    auto step = [&](int s, bool cut) {
+        const uint8_t *X = lds + (s & 1) * PB_STAGE, *W = X + PB_X + wave * 4096, *S = X + PB_X + PB_W;
         i32x8v a[4];
+        int sa[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) a[j] = code_reg(w.c[j]);
+        for (int j = 0; j < 4; ++j) {
+            uint4 v = *reinterpret_cast<const uint4 *>(W + chunk_at(16 * j + li, lg));
+            if (cut && lg >= 2) v = make_uint4(0, 0, 0, 0);    // columns past K
+            a[j] = code_reg(v);
+            sa[j] = (int)(reinterpret_cast<const uint32_t *>(S)[64 * wave + 16 * j + li] >> (8 * lg));
+        }
 #pragma unroll
         for (int f = 0; f < MF; ++f) {
-            const int r = 16 * f + li, c = 4 * (s & 1) + lg;
-            const i32x8v b = code_reg(*reinterpret_cast<const uint4 *>(L + r * 128 + 16 * (c ^ ((r >> 1) & 7))));
-            const uint32_t xsf = f < 4 ? xs.x : xs.y;
+            const i32x8v b = code_reg(*reinterpret_cast<const uint4 *>(X + chunk_at(16 * f + li, lg)));
+            const int sb = (int)(reinterpret_cast<const uint32_t *>(S + 4 * PB_N)[16 * f + li] >> (8 * lg));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                switch (f & 3) {                          // the scale's byte is part of the instruction
-                case 0: acc[j][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[j], b, acc[j][f], 4, 4, 0, (int)w.s[j], 0, (int)xsf); break;
-                case 1: acc[j][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[j], b, acc[j][f], 4, 4, 0, (int)w.s[j], 1, (int)xsf); break;
-                case 2: acc[j][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[j], b, acc[j][f], 4, 4, 0, (int)w.s[j], 2, (int)xsf); break;
-                default: acc[j][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[j], b, acc[j][f], 4, 4, 0, (int)w.s[j], 3, (int)xsf); break;
-                }
-            }
+            for (int j = 0; j < 4; ++j)
+                acc[j][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[j], b, acc[j][f], 4, 4, 0, sa[j], 0, sb);
         }
     };
 
+    uint32_t ws4 = scales4(wsc, 0, half && steps == 1), xs4 = scales4(xsc, 0, half && steps == 1);
     issue(0);
-    WStep w0, w1;
-    wload(w0, 0);
-    for (int st = 0; st < stages; ++st) {
-        // this stage's loads have landed in every wave, and every wave has left the other buffer
+    put_scales(0, ws4, xs4);
+    for (int s = 0; s < steps; ++s) {
+        // stage s has landed in every wave, and every wave has left the other buffer
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (st + 1 < stages) issue(st + 1);
-        wload(w1, 2 * st + 1);
-        step(w0, 2 * st);
-        wload(w0, 2 * st + 2);
-        if (2 * st + 1 < steps) step(w1, 2 * st + 1);
+        const bool more = s + 1 < steps;
+        if (more) {
+            ws4 = scales4(wsc, s + 1, half && s + 2 == steps);
+            xs4 = scales4(xsc, s + 1, half && s + 2 == steps);
+            issue(s + 1);
+        }
+        if (live) step(s, half && s + 1 == steps);
+        if (more) put_scales(s + 1, ws4, xs4);
     }
 
     // ---- epilogue: lane l, element i of acc[j][f] is output 16 j + 4 (l / 16) + i of row 16 f + l % 16
@@ -372,7 +401,7 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
 
 __global__ __launch_bounds__(256, 2) void product_mx4_kernel(Mx4Product p, int ntiles)
 {
-    extern __shared__ __attribute__((aligned(16))) uint8_t mx4_lds[];
+    __shared__ __attribute__((aligned(16))) uint8_t mx4_lds[2 * PB_STAGE];
     const int b = blockIdx.x, mt = b / ntiles, nt = b - mt * ntiles;
     const Tile t = find_tile(p, mt, PB_M, threadIdx.x & 63);
     if (t.rows < 1) return;
@@ -417,129 +446,171 @@ __device__ __forceinline__ void cut_f32x8(const float *v, bf16x8 (&terms)[3])
     terms[2] = c.v;
 }
 
-template <int XK, int TN, int MT, int NW>
-__global__ __launch_bounds__(64 * NW) void product_wide_kernel(Mx4Product p)
+// A block takes `iters` such sets of weight tiles, one after another.  A wave's share of K runs in
+// batches of U steps of 128 columns; a batch's weights and scales are asked for while the batch
+// before it (of the same tiles or of the set before) is multiplied, so TN x U KB are in flight per
+// wave all the time.
+template <int XK, int TN, int MT, int NW, int U>
+__global__ __launch_bounds__(64 * NW) void product_wide_kernel(Mx4Product p, int iters)
 {
-    constexpr int NTERM = XTerms<XK>::N;
+    constexpr int NTERM = XTerms<XK>::N, XB = XK == X_F32 ? 4 : 2;
     __shared__ float red[NW][TN * 256];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, li = lane & 15, lg = lane >> 4;
-    const Tile t = find_tile(p, blockIdx.y, 1 << 30, lane);
+    const Tile t = find_slot(p, blockIdx.y, lane);
     if (t.rows < 1) return;
     const bool glu = p.act == ACT_SWIGLU;
     const int F = p.N >> 1, NO = glu ? F : p.N;
     const int TO = glu ? TN / 2 : TN;                      // output tiles
     const int KB = p.K >> 1, KSC = p.K >> 5, steps = (p.K + 127) >> 7;
-    const int n0 = blockIdx.x * TO * 16;
+    const int per = (steps + NW - 1) / NW, s0 = wave * per, s1 = min(steps, s0 + per);
+    const int nbatch = (per + U - 1) / U;                  // the same in every wave
+    const int nset0 = blockIdx.x * iters, nsets = min(iters, (NO + 16 * TO - 1) / (16 * TO) - nset0);
 
-    const uint8_t *wp[TN], *sp[TN];
+    struct Batch {
+        uint4 w[U][TN];
+        uint32_t s[U][TN];
+    };
+    auto load = [&](Batch &b, int it, int ib) {
+        const int n0 = (nset0 + it) * TO * 16;
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-        int n;
-        if (glu) {
-            const int f = min(n0 + 16 * (j % (TN / 2)) + li, F - 1);
-            n = j < TN / 2 ? f : F + f;
-        } else {
-            n = min(n0 + 16 * j + li, p.N - 1);
+        for (int j = 0; j < TN; ++j) {
+            int n;
+            if (glu) {
+                const int f = min(n0 + 16 * (j % (TN / 2)) + li, F - 1);
+                n = j < TN / 2 ? f : F + f;
+            } else {
+                n = min(n0 + 16 * j + li, p.N - 1);
+            }
+            const size_t row = (size_t)t.g * p.N + n;
+            const uint8_t *wp = p.w + row * KB + 16 * lg, *sp = p.ws + row * KSC + lg;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int s = s0 + ib * U + u;
+                b.w[u][j] = make_uint4(0, 0, 0, 0);
+                b.s[u][j] = 127;
+                if (s < s1 && 128 * s + 32 * lg < p.K) {
+                    b.w[u][j] = *reinterpret_cast<const uint4 *>(wp + (size_t)s * 64);
+                    b.s[u][j] = sp[s * 4];
+                }
+            }
         }
-        const size_t row = (size_t)t.g * p.N + n;
-        wp[j] = p.w + row * KB + 16 * lg;
-        sp[j] = p.ws + row * KSC + lg;
-    }
+    };
 
     for (int r0 = 0; r0 < t.rows; r0 += 16 * MT) {
-        f32x4 acc[TN][MT];
         const uint8_t *xp[MT];
         bool in[MT];
+        Batch next;
+        load(next, 0, 0);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const int r = r0 + 16 * m + li;
             in[m] = r < t.rows;
             const size_t src = source_row(p, t.row0 + min(r, t.rows - 1));
-            xp[m] = static_cast<const uint8_t *>(p.x) + (src * p.K + 32 * lg) * (XK == X_F32 ? 4 : 2);
-#pragma unroll
-            for (int j = 0; j < TN; ++j) acc[j][m] = zero4();
+            xp[m] = static_cast<const uint8_t *>(p.x) + (src * p.K + 32 * lg) * XB;
         }
-        for (int s = wave; s < steps; s += NW) {
-            const bool kin = 128 * s + 32 * lg < p.K;
-            uint4 w[TN];
-            float sc[TN];
+        for (int it = 0; it < nsets; ++it) {
+            f32x4 acc[TN][MT];
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                w[j] = make_uint4(0, 0, 0, 0);
-                uint32_t sb = 127;
-                if (kin) {
-                    w[j] = *reinterpret_cast<const uint4 *>(wp[j] + (size_t)s * 64);
-                    sb = sp[j][s * 4];
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int j = 0; j < TN; ++j) acc[j][m] = zero4();
+            for (int ib = 0; ib < nbatch; ++ib) {
+                const Batch cur = next;
+                const bool last = ib + 1 == nbatch;
+                if (!last || it + 1 < nsets) load(next, last ? it + 1 : it, last ? 0 : ib + 1);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int s = s0 + ib * U + u;
+                    if (s >= s1) break;
+                    const bool kin = 128 * s + 32 * lg < p.K;
+                    float sc[TN];
+#pragma unroll
+                    for (int j = 0; j < TN; ++j) sc[j] = e8m0_f32(cur.s[u][j]);
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        if (MT > 1 && r0 + 16 * m >= t.rows) break;
+                        bf16x8 xt[4][NTERM];
+                        if constexpr (XK == X_F32) {
+                            float v[4][8] = {};
+                            if (in[m] && kin) {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) {
+                                    const float4 *g = reinterpret_cast<const float4 *>(xp[m] + ((size_t)s * 128 + 8 * q) * 4);
+                                    const float4 a = g[0], b = g[1];
+                                    v[q][0] = a.x; v[q][1] = a.y; v[q][2] = a.z; v[q][3] = a.w;
+                                    v[q][4] = b.x; v[q][5] = b.y; v[q][6] = b.z; v[q][7] = b.w;
+                                }
+                            }
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) cut_f32x8(v[q], xt[q]);
+                        } else {
+                            U4 v[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) v[q].u = make_uint4(0, 0, 0, 0);
+                            if (in[m] && kin) {
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    v[q].u = *reinterpret_cast<const uint4 *>(xp[m] + ((size_t)s * 128 + 8 * q) * 2);
+                            }
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) xt[q][0] = v[q].v;
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int j = 0; j < TN; ++j) {
+                                const uint4 &wj = cur.w[u][j];
+                                const uint32_t c = q == 0 ? wj.x : q == 1 ? wj.y : q == 2 ? wj.z : wj.w;
+                                const bf16x8 wb = mx4_bf16x8(c, sc[j]);
+#pragma unroll
+                                for (int k = NTERM - 1; k >= 0; --k) acc[j][m] = mfma16x16x32_bf16(wb, xt[q][k], acc[j][m]);
+                            }
+                    }
                 }
-                sc[j] = e8m0_f32(sb);
             }
+            // ---- the waves' sums, then the activation; element i of a lane is weight row 4 lg + i of x row li
+            const int n0 = (nset0 + it) * TO * 16;
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                if (MT > 1 && r0 + 16 * m >= t.rows) break;
+                if (r0 + 16 * m >= t.rows) break;
+                if (m > 0 || it > 0 || r0 > 0) lds_barrier();
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    bf16x8 xt[NTERM];
-                    if constexpr (XK == X_F32) {
-                        float v[8] = {};
-                        if (in[m] && kin) {
-                            const float4 *g = reinterpret_cast<const float4 *>(xp[m] + ((size_t)s * 128 + 8 * q) * 4);
-                            const float4 a = g[0], b = g[1];
-                            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-                            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-                        }
-                        cut_f32x8(v, xt);
-                    } else {
-                        U4 u;
-                        u.u = make_uint4(0, 0, 0, 0);
-                        if (in[m] && kin) u.u = *reinterpret_cast<const uint4 *>(xp[m] + ((size_t)s * 128 + 8 * q) * 2);
-                        xt[0] = u.v;
+                for (int j = 0; j < TN; ++j)
+                    *reinterpret_cast<f32x4 *>(&red[wave][j * 256 + li * 16 + 4 * lg]) = acc[j][m];
+                lds_barrier();
+                const int rows = min(16, t.rows - r0 - 16 * m);
+                for (int i = tid; i < rows * 16 * TO; i += 64 * NW) {
+                    const int r = i / (16 * TO), n = i - r * 16 * TO;
+                    const int at = (n >> 4) * 256 + r * 16 + (n & 15);
+                    float v = 0.f, u = 0.f;
+#pragma unroll
+                    for (int k = 0; k < NW; ++k) {
+                        v += red[k][at];
+                        if (glu) u += red[k][at + (TN / 2) * 256];
                     }
-#pragma unroll
-                    for (int j = 0; j < TN; ++j) {
-                        const uint32_t c = q == 0 ? w[j].x : q == 1 ? w[j].y : q == 2 ? w[j].z : w[j].w;
-                        const bf16x8 wb = mx4_bf16x8(c, sc[j]);
-#pragma unroll
-                        for (int k = NTERM - 1; k >= 0; --k) acc[j][m] = mfma16x16x32_bf16(wb, xt[k], acc[j][m]);
-                    }
+                    if (n0 + n < NO)
+                        store1(p, (size_t)(t.row0 + r0 + 16 * m + r) * NO + n0 + n, glu ? silu_f32(v) * u : activate(v, p.act));
                 }
-            }
-        }
-        // ---- the waves' sums, then the activation; element i of a lane is weight row 4 lg + i of x row li
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            if (r0 + 16 * m >= t.rows) break;
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-                *reinterpret_cast<f32x4 *>(&red[wave][j * 256 + li * 16 + 4 * lg]) = acc[j][m];
-            __syncthreads();
-            for (int i = tid; i < TO * 256; i += 64 * NW) {
-                const int n = i % (16 * TO), r = i / (16 * TO);
-                const int at = (n >> 4) * 256 + r * 16 + (n & 15);
-                float v = 0.f, u = 0.f;
-#pragma unroll
-                for (int k = 0; k < NW; ++k) {
-                    v += red[k][at];
-                    if (glu) u += red[k][at + (TN / 2) * 256];
-                }
-                if (r0 + 16 * m + r < t.rows && n0 + n < NO)
-                    store1(p, (size_t)(t.row0 + r0 + 16 * m + r) * NO + n0 + n, glu ? silu_f32(v) * u : activate(v, p.act));
             }
         }
     }
 }
 
-template <int XK, int TN>
+template <int XK, int TN, int NW, int U>
 hipError_t launch_wide(const Mx4Product &p, hipStream_t s)
 {
-    constexpr int NW = 4;
     const int TO = p.act == ACT_SWIGLU ? TN / 2 : TN;
     const int NO = p.act == ACT_SWIGLU ? p.N / 2 : p.N;
     const int rows = p.Pr + p.S * p.T;
     const int G = p.offsets ? p.E + p.S : 1;
-    const dim3 grid((NO + 16 * TO - 1) / (16 * TO), rows < G ? rows : G);
-    if (rows <= 16) product_wide_kernel<XK, TN, 1, NW><<<grid, 64 * NW, 0, s>>>(p);
-    else product_wide_kernel<XK, TN, 4, NW><<<grid, 64 * NW, 0, s>>>(p);
+    const int slots = rows < G ? rows : G, sets = (NO + 16 * TO - 1) / (16 * TO);
+    static const int BL = getenv("WB") ? atoi(getenv("WB")) : 2048;
+    int iters = (int)((long long)sets * slots / BL);
+    iters = iters < 1 ? 1 : (iters > sets ? sets : iters);
+    const dim3 grid((sets + iters - 1) / iters, slots);
+    // 16 rows at a time where groups hold few, 64 where they hold many
+    if (rows <= 16 || rows < 8 * G) product_wide_kernel<XK, TN, 1, NW, U><<<grid, 64 * NW, 0, s>>>(p, iters);
+    else product_wide_kernel<XK, TN, 4, NW, U><<<grid, 64 * NW, 0, s>>>(p, iters);
     return hipGetLastError();
 }
 
@@ -569,20 +640,18 @@ hipError_t launch_quantize_mx4(const void *v, int xtype, int rows, int cols, uin
 hipError_t launch_product_mx4(const Mx4Product &p, hipStream_t s)
 {
     ProfScope prof(K_PRODUCT_MX4, s);
-    if (p.xtype == X_F32) return launch_wide<X_F32, 4>(p, s);
-    if (p.xtype == X_BF16) return launch_wide<X_BF16, 2>(p, s);
+    if (p.xtype != X_MX4) {
+        static const int var = getenv("WV") ? atoi(getenv("WV")) : 0;
+#define V(i, TN, NW, U) if (var == i) return p.xtype == X_F32 ? launch_wide<X_F32, TN, NW, U>(p, s) : launch_wide<X_BF16, TN, NW, U>(p, s);
+        V(0, 4, 4, 2) V(1, 4, 8, 1) V(2, 4, 4, 1) V(3, 8, 4, 1) V(4, 4, 2, 2) V(5, 8, 2, 1) V(6, 8, 8, 1) V(7, 4, 1, 2)
+#undef V
+    }
     const int NO = p.act == ACT_SWIGLU ? p.N / 2 : p.N;
     const int per = p.act == ACT_SWIGLU ? PB_N / 2 : PB_N;
     const int ntiles = (NO + per - 1) / per;
     const int rows = p.Pr + p.S * p.T, G = p.offsets ? p.E + p.S : 1;
     const int mtiles = rows / PB_M + (rows < G ? rows : G);        // at least the sum of the groups' tiles
-    const int lds = 2 * PB_M * (PB_KS / 2) + 512 * ((p.K + 127) / 128);
-    if (lds > 64 * 1024) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void *>(product_mx4_kernel),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        if (e != hipSuccess) return e;
-    }
-    product_mx4_kernel<<<(unsigned)mtiles * ntiles, 256, lds, s>>>(p, ntiles);
+    product_mx4_kernel<<<(unsigned)mtiles * ntiles, 256, 0, s>>>(p, ntiles);
     return hipGetLastError();
 }
 
