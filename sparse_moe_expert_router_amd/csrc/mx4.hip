@@ -96,38 +96,83 @@ __device__ __forceinline__ int wave_scan_incl(int v, int lane)
     return v;
 }
 
-// Tile number `tile` when every group's rows are cut into tiles of `bm`.  Offsets are clamped into
-// [0, Pr] and taken as ascending, so no value of theirs leads outside the rows.
-__device__ __forceinline__ Tile find_tile(const Mx4Product &p, int tile, int bm, int lane)
+// The groups' rows, 64 groups per register, their loads all in flight together.  Offsets are clamped
+// into [0, Pr] and taken as ascending, so no value of theirs leads outside the rows.
+constexpr int GROUP_REGS = (MAX_E + MAX_SHARED + 63) / 64;
+struct Groups {
+    int lo[GROUP_REGS], hi[GROUP_REGS];
+};
+__device__ __forceinline__ Groups load_groups(const Mx4Product &p, int lane)
 {
-    if (p.offsets == nullptr) {
-        const int r0 = tile * bm;
-        return Tile{0, r0, min(bm, p.Pr - r0)};
-    }
+    Groups q;
     const int G = p.E + p.S;
-    int before = 0;
-    for (int c = 0; c < G; c += 64) {
-        const int g = c + lane;
-        int lo = 0, hi = 0;
-        if (g < p.E) {
-            lo = min(max(p.offsets[g], 0), p.Pr);
-            hi = min(max(p.offsets[g + 1], lo), p.Pr);
-        } else if (g < G) {
-            lo = p.Pr + (g - p.E) * p.T;
-            hi = lo + p.T;
+#pragma unroll
+    for (int c = 0; c < GROUP_REGS; ++c) {
+        const int g = 64 * c + lane;
+        q.lo[c] = q.hi[c] = 0;
+        if (64 * c < G) {
+            if (g < p.E) {
+                q.lo[c] = p.offsets[g];
+                q.hi[c] = p.offsets[g + 1];
+            } else if (g < G) {
+                q.lo[c] = p.Pr + (g - p.E) * p.T;
+                q.hi[c] = q.lo[c] + p.T;
+            }
         }
-        const int nt = (hi - lo + bm - 1) / bm;
-        const int incl = wave_scan_incl(nt, lane);
-        const unsigned long long m = __ballot(before + incl > tile);
-        if (m) {
-            const int at = __ffsll((long long)m) - 1;
-            const int t = tile - before - __shfl(incl - nt, at, WAVE);
-            const int glo = __shfl(lo, at, WAVE), ghi = __shfl(hi, at, WAVE);
-            return Tile{c + at, glo + t * bm, min(bm, ghi - glo - t * bm)};
-        }
-        before += __shfl(incl, 63, WAVE);
     }
-    return Tile{0, 0, 0};
+#pragma unroll
+    for (int c = 0; c < GROUP_REGS; ++c)
+        if (64 * c + lane < p.E) {
+            q.lo[c] = min(max(q.lo[c], 0), p.Pr);
+            q.hi[c] = min(max(q.hi[c], q.lo[c]), p.Pr);
+        }
+    return q;
+}
+
+// Block b's tile when every group's rows are cut into tiles of `bm` and the weight rows into
+// `ntiles`.  Blocks go to the 8 XCDs in turn, so each XCD takes a contiguous eighth of the tiles,
+// weight tiles running fastest: the row tiles of one group, which read the same weights, and the
+// weight tiles of one row tile, which read the same rows, meet in one L2.
+__device__ __forceinline__ Tile find_tile(const Mx4Product &p, int b, int bm, int ntiles, int lane, int &nt)
+{
+    const int G = p.E + p.S;
+    Groups q;
+    int incl[GROUP_REGS], before[GROUP_REGS], total = 0;
+    if (p.offsets == nullptr) {
+        total = (p.Pr + bm - 1) / bm;
+    } else {
+        q = load_groups(p, lane);
+#pragma unroll
+        for (int c = 0; c < GROUP_REGS; ++c)
+            if (64 * c < G) incl[c] = wave_scan_incl((q.hi[c] - q.lo[c] + bm - 1) / bm, lane);
+#pragma unroll
+        for (int c = 0; c < GROUP_REGS; ++c) {
+            before[c] = total;
+            if (64 * c < G) total += __builtin_amdgcn_readlane(incl[c], 63);
+        }
+    }
+    const int live = total * ntiles, x = b & 7, i = b >> 3;
+    const int j0 = (int)((long long)live * x / 8), j1 = (int)((long long)live * (x + 1) / 8);
+    Tile t{0, 0, 0};
+    nt = 0;
+    if (j0 + i >= j1) return t;
+    const int tile = (j0 + i) / ntiles;
+    nt = j0 + i - tile * ntiles;
+    if (p.offsets == nullptr) return Tile{0, tile * bm, min(bm, p.Pr - tile * bm)};
+#pragma unroll
+    for (int c = 0; c < GROUP_REGS; ++c) {
+        if (64 * c >= G) continue;
+        const unsigned long long m = __ballot(before[c] + incl[c] > tile);
+        if (m && before[c] <= tile) {
+            const int at = __ffsll((long long)m) - 1;
+            const int lo = __builtin_amdgcn_readlane(q.lo[c], at), hi = __builtin_amdgcn_readlane(q.hi[c], at);
+            const int first = before[c] + __builtin_amdgcn_readlane(incl[c], at) - (hi - lo + bm - 1) / bm;
+            const int r0 = lo + (tile - first) * bm;
+            t = Tile{64 * c + at, r0, min(bm, hi - r0)};
+            break;
+        }
+    }
+    return t;
 }
 
 // The `slot`-th group that holds rows, all of its rows.  A group holds rows or not, so a ballot and
@@ -136,41 +181,22 @@ __device__ __forceinline__ Tile find_slot(const Mx4Product &p, int slot, int lan
 {
     if (p.offsets == nullptr) return Tile{0, 0, slot == 0 ? p.Pr : 0};
     const int G = p.E + p.S;
-    constexpr int NC = (MAX_E + MAX_SHARED + 63) / 64;
-    int lo[NC], hi[NC];
-#pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        const int g = 64 * c + lane;
-        lo[c] = hi[c] = 0;
-        if (64 * c < G) {
-            if (g < p.E) {
-                lo[c] = p.offsets[g];
-                hi[c] = p.offsets[g + 1];
-            } else if (g < G) {
-                lo[c] = p.Pr + (g - p.E) * p.T;
-                hi[c] = lo[c] + p.T;
-            }
-        }
-    }
+    const Groups q = load_groups(p, lane);
     Tile t{0, 0, 0};
     int before = 0;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-        if (64 * c < G) {
-            if (64 * c + lane < p.E) {
-                lo[c] = min(max(lo[c], 0), p.Pr);
-                hi[c] = min(max(hi[c], lo[c]), p.Pr);
-            }
-            const unsigned long long m = __ballot(hi[c] > lo[c]);
-            const int n = __popcll(m);
-            if (slot >= before && slot < before + n) {
-                const unsigned long long below = (1ull << lane) - 1;
-                const unsigned long long at = __ballot(((m >> lane) & 1) && __popcll(m & below) == slot - before);
-                const int l = __ffsll((long long)at) - 1;
-                t = Tile{64 * c + l, __shfl(lo[c], l, WAVE), __shfl(hi[c], l, WAVE) - __shfl(lo[c], l, WAVE)};
-            }
-            before += n;
+    for (int c = 0; c < GROUP_REGS; ++c) {
+        if (64 * c >= G) continue;
+        const unsigned long long m = __ballot(q.hi[c] > q.lo[c]);
+        const int n = __popcll(m);
+        if (slot >= before && slot < before + n) {
+            const unsigned long long below = (1ull << lane) - 1;
+            const unsigned long long at = __ballot(((m >> lane) & 1) && __popcll(m & below) == slot - before);
+            const int l = __ffsll((long long)at) - 1;
+            const int lo = __builtin_amdgcn_readlane(q.lo[c], l);
+            t = Tile{64 * c + l, lo, __builtin_amdgcn_readlane(q.hi[c], l) - lo};
         }
+        before += n;
     }
     return t;
 }
@@ -225,8 +251,11 @@ __device__ __forceinline__ void store4(const Mx4Product &p, int row, int n0, int
 // (16 accesses per KB), double-buffered in stages of 128 columns.
 
 constexpr int PB_M = 128, PB_N = 256;                  // rows, weight rows of a block
-constexpr int PB_X = PB_M * 64, PB_W = PB_N * 64;      // bytes of a stage's codes (128 columns)
-constexpr int PB_STAGE = PB_X + PB_W + 4 * (PB_M + PB_N);   // and 4 scale bytes per row
+constexpr int PB_XST = PB_M * 64, PB_WST = PB_N * 64;  // bytes of a stage's codes (128 columns)
+constexpr int PB_XBUF = 2, PB_WBUF = 3;                // weights come from HBM, rows mostly from L2
+constexpr int PB_WLOADS = 4;                           // load instructions of a wave per weight stage
+constexpr int PB_SST = 16 * (PB_M + PB_N);             // 16 scales (512 columns) of every row
+constexpr int PB_LDS = PB_WBUF * PB_WST + PB_XBUF * PB_XST + 2 * PB_SST;
 
 __device__ __forceinline__ void lds_dma16(const void *g, uint32_t lds)
 {
@@ -251,14 +280,19 @@ __device__ __forceinline__ i32x8v code_reg(const uint4 &v)
 // fragment read at once fall on different banks.
 __device__ __forceinline__ int chunk_at(int r, int c) { return r * 64 + 16 * (c ^ ((r >> 2) & 3)); }
 
-// The four scale bytes of columns 128 s .. of a row (`row`: its scales), 1 for the missing ones.
-// Rows of scales start at even addresses only.
-__device__ __forceinline__ uint32_t scales4(const uint8_t *row, int s, bool half)
+// Scales 16 q .. 16 q + 15 of a row (`row`: its scales, n in all), 1 for those past the end.  Rows of
+// scales start at even addresses only.
+__device__ __forceinline__ uint4 scales16(const uint8_t *row, int q, int n)
 {
-    uint32_t v;
-    if (half) return *reinterpret_cast<const uint16_t *>(row + 4 * s) | 0x7F7F0000u;
-    __builtin_memcpy(&v, __builtin_assume_aligned(row + 4 * s, 2), 4);
-    return v;
+    uint4 v;
+    if (16 * q + 16 <= n) {
+        __builtin_memcpy(&v, __builtin_assume_aligned(row + 16 * q, 2), 16);
+        return v;
+    }
+    uint32_t h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = 16 * q + 2 * i < n ? *reinterpret_cast<const uint16_t *>(row + 16 * q + 2 * i) : 0x7F7Fu;
+    return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
 }
 
 // MG: 32-row groups of the tile that hold rows.
@@ -282,35 +316,37 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
     };
     const bool live = (glu ? nt * 128 + wave * 32 : nt * 256 + wave * 64) < NO;
 
-    // ---- sources: 4 lanes read a row's 64 bytes; instruction i of a wave fills 16 rows
-    constexpr int XI = (MF + 3) / 4;                      // x instructions of a wave
+    // ---- sources: 4 lanes read a row's 64 bytes; instruction i of a wave fills 16 rows.  Rows past the
+    // tile's or the matrix's end read the last one, so that every wave issues the same loads.
+    constexpr int XI = (MF + 3) / 4;                      // x code instructions of a wave
     const uint8_t *wsrc[4], *xsrc[XI];
     const int drow = lane >> 2, dchunk = 16 * ((lane & 3) ^ ((lane >> 4) & 3));   // (row >> 2) & 3 of row = lane / 4
+    auto x_row = [&](int r) { return (size_t)source_row(p, t.row0 + min(r, t.rows - 1)); };
 #pragma unroll
     for (int i = 0; i < 4; ++i) wsrc[i] = p.w + weight_row(64 * wave + 16 * i + drow) * KB;
 #pragma unroll
-    for (int i = 0; i < XI; ++i) {
-        const int r = 16 * (wave + 4 * i) + drow;
-        xsrc[i] = static_cast<const uint8_t *>(p.x) + (size_t)source_row(p, t.row0 + min(r, t.rows - 1)) * KB;
-    }
-    const uint8_t *wsc = p.ws + weight_row(tid) * KSC;    // thread r: scales of weight row r, of row r
-    const uint8_t *xsc = p.xs + (size_t)source_row(p, t.row0 + min(tid & (PB_M - 1), t.rows - 1)) * KSC;
+    for (int i = 0; i < XI; ++i) xsrc[i] = static_cast<const uint8_t *>(p.x) + x_row(16 * (wave + 4 * i) + drow) * KB;
+    // thread r: the scales of weight row r and (the first 128) of row r
+    const uint8_t *wsc = p.ws + weight_row(tid) * KSC;
+    const uint8_t *xsc = p.xs + x_row(tid & (PB_M - 1)) * KSC;
 
-    auto issue = [&](int s) {
-        const uint32_t L = lds_addr(lds + (s & 1) * PB_STAGE);
+    uint8_t *xlds = lds + PB_WBUF * PB_WST, *slds = xlds + PB_XBUF * PB_XST;
+    auto issue_w = [&](int s, int buf) {
+        const uint32_t L = lds_addr(lds + buf * PB_WST);
+        const int off = min(min(s, steps - 1) * 64 + dchunk, KB - 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lds_dma16(wsrc[i] + off, L + (4 * wave + i) * 1024);
+    };
+    auto issue_x = [&](int s) {
+        const uint32_t L = lds_addr(xlds + (s & 1) * PB_XST);
         const int off = min(s * 64 + dchunk, KB - 16);
 #pragma unroll
-        for (int i = 0; i < XI; ++i)
-            if (wave + 4 * i < MF) lds_dma16(xsrc[i] + off, L + (wave + 4 * i) * 1024);
-        if (live) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) lds_dma16(wsrc[i] + off, L + PB_X + (4 * wave + i) * 1024);
-        }
+        for (int i = 0; i < XI; ++i) lds_dma16(xsrc[i] + off, L + (wave + 4 * i) * 1024);
     };
-    auto put_scales = [&](int s, uint32_t w, uint32_t x) {
-        uint8_t *S = lds + (s & 1) * PB_STAGE + PB_X + PB_W;
-        reinterpret_cast<uint32_t *>(S)[tid] = w;
-        if (tid < PB_M) reinterpret_cast<uint32_t *>(S + 4 * PB_N)[tid] = x;
+    auto put_scales = [&](int q, const uint4 &w, const uint4 &x) {
+        uint4 *S = reinterpret_cast<uint4 *>(slds + (q & 1) * PB_SST);
+        S[tid] = w;
+        if (tid < PB_M) S[PB_N + tid] = x;
     };
 
     f32x4 acc[4][MF];
@@ -319,42 +355,58 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
 #pragma unroll
         for (int f = 0; f < MF; ++f) acc[j][f] = zero4();
 
-    auto step = [&](int s, bool cut) {
-        const uint8_t *X = lds + (s & 1) * PB_STAGE, *W = X + PB_X + wave * 4096, *S = X + PB_X + PB_W;
+    auto step = [&](int s, int buf, bool cut) {
+        const uint8_t *X = xlds + (s & 1) * PB_XST, *W = lds + buf * PB_WST;
+        const uint32_t *S = reinterpret_cast<const uint32_t *>(slds + ((s >> 2) & 1) * PB_SST) + (s & 3);
+        const uint32_t *WS = S + 4 * (64 * wave + li), *XS = S + 4 * (PB_N + li);
+        const int sh = 8 * lg;
         i32x8v a[4];
         int sa[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            uint4 v = *reinterpret_cast<const uint4 *>(W + chunk_at(16 * j + li, lg));
+            uint4 v = *reinterpret_cast<const uint4 *>(W + wave * 4096 + chunk_at(16 * j + li, lg));
             if (cut && lg >= 2) v = make_uint4(0, 0, 0, 0);    // columns past K
             a[j] = code_reg(v);
-            sa[j] = (int)(reinterpret_cast<const uint32_t *>(S)[64 * wave + 16 * j + li] >> (8 * lg));
+            sa[j] = (int)(WS[64 * j] >> sh);
         }
 #pragma unroll
         for (int f = 0; f < MF; ++f) {
             const i32x8v b = code_reg(*reinterpret_cast<const uint4 *>(X + chunk_at(16 * f + li, lg)));
-            const int sb = (int)(reinterpret_cast<const uint32_t *>(S + 4 * PB_N)[16 * f + li] >> (8 * lg));
+            const int sb = (int)(XS[64 * f] >> sh);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 acc[j][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[j], b, acc[j][f], 4, 4, 0, sa[j], 0, sb);
         }
     };
 
-    uint32_t ws4 = scales4(wsc, 0, half && steps == 1), xs4 = scales4(xsc, 0, half && steps == 1);
-    issue(0);
-    put_scales(0, ws4, xs4);
+    // Weights are asked for two steps ahead, x one step ahead.  At the top of step s the newest
+    // loads in flight are the weights of step s + 1; everything older has to be there.  Every step
+    // issues the same number of loads (past the end the last step's again), so the count holds.
+    // Scales go through registers, 16 of a row at a time: asked for at the first of four steps, put
+    // into the other LDS buffer at the last.
+    uint4 sw = scales16(wsc, 0, KSC), sx = scales16(xsc, 0, KSC);
+    issue_x(0);
+    issue_w(0, 0);
+    issue_w(1, 1);
+    put_scales(0, sw, sx);
+    int buf = 0;
     for (int s = 0; s < steps; ++s) {
-        // stage s has landed in every wave, and every wave has left the other buffer
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        const bool more = s + 1 < steps;
-        if (more) {
-            ws4 = scales4(wsc, s + 1, half && s + 2 == steps);
-            xs4 = scales4(xsc, s + 1, half && s + 2 == steps);
-            issue(s + 1);
+        // stage s has landed in every wave, and every wave has left the buffers filled next
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(PB_WLOADS) : "memory");
+        const int q = (s >> 2) + 1;
+        const bool more = 16 * q < KSC;
+        if ((s & 3) == 0 && more) {
+            sw = scales16(wsc, q, KSC);
+            sx = scales16(xsc, q, KSC);
         }
-        if (live) step(s, half && s + 1 == steps);
-        if (more) put_scales(s + 1, ws4, xs4);
+        if (s + 1 < steps) issue_x(s + 1);
+        issue_w(s + 2, buf == 0 ? 2 : buf - 1);
+        if (live) step(s, buf, half && s + 1 == steps);
+        if ((s & 3) == 3 && more) put_scales(q, sw, sx);
+        buf = buf == 2 ? 0 : buf + 1;
     }
+    // no load may still be writing this block's LDS when it exits
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 
     // ---- epilogue: lane l, element i of acc[j][f] is output 16 j + 4 (l / 16) + i of row 16 f + l % 16
     if (!live) return;
@@ -401,9 +453,9 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
 
 __global__ __launch_bounds__(256, 2) void product_mx4_kernel(Mx4Product p, int ntiles)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t mx4_lds[2 * PB_STAGE];
-    const int b = blockIdx.x, mt = b / ntiles, nt = b - mt * ntiles;
-    const Tile t = find_tile(p, mt, PB_M, threadIdx.x & 63);
+    __shared__ __attribute__((aligned(16))) uint8_t mx4_lds[PB_LDS];
+    int nt;
+    const Tile t = find_tile(p, blockIdx.x, PB_M, ntiles, threadIdx.x & 63, nt);
     if (t.rows < 1) return;
     switch ((t.rows + 31) >> 5) {
     case 1: product_tile<1>(p, t, nt, mx4_lds); break;
@@ -651,7 +703,7 @@ hipError_t launch_product_mx4(const Mx4Product &p, hipStream_t s)
     const int ntiles = (NO + per - 1) / per;
     const int rows = p.Pr + p.S * p.T, G = p.offsets ? p.E + p.S : 1;
     const int mtiles = rows / PB_M + (rows < G ? rows : G);        // at least the sum of the groups' tiles
-    product_mx4_kernel<<<(unsigned)mtiles * ntiles, 256, 0, s>>>(p, ntiles);
+    product_mx4_kernel<<<((unsigned)mtiles * ntiles + 7) / 8 * 8, 256, 0, s>>>(p, ntiles);
     return hipGetLastError();
 }
 
