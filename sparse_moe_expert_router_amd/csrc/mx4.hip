@@ -10,6 +10,8 @@
 #include <hip/hip_runtime.h>
 
 #include <cstdlib>
+#include <type_traits>
+
 #include "moe_launch.hpp"
 #include "mx4_dev.hpp"
 
@@ -215,30 +217,21 @@ __device__ __forceinline__ float activate(float v, int act)
     return act == ACT_RELU2 ? (v != v ? v : r * r) : v;
 }
 
-__device__ __forceinline__ void store1(const Mx4Product &p, size_t at, float v)
+// silu(g) = g / (1 + 2^(-g log2 e)).  The exponent is split in two floats, so its rounding does not
+// grow with |g|; exp and reciprocal instructions are good to 1 ulp.
+__device__ __forceinline__ float silu_fast(float g)
 {
-    if (p.otype == X_F32) static_cast<float *>(p.out)[at] = v;
-    else static_cast<uint16_t *>(p.out)[at] = __builtin_bit_cast(uint16_t, (__bf16)v);
+    const float x = __builtin_amdgcn_fmed3f(-g, -88.5f, 88.5f);      // 2^127.7: sums and products stay finite
+    const float hi = x * 1.44269504f, lo = fmaf(x, 1.44269504f, -hi) + x * 1.9259630e-8f;
+    const float e = __builtin_amdgcn_exp2f(hi);
+    return g * __builtin_amdgcn_rcpf(1.f + fmaf(e, lo * 0.69314718f, e));
 }
 
-// four consecutive outputs from n0 on, of which those below N exist
-__device__ __forceinline__ void store4(const Mx4Product &p, int row, int n0, int NO, const float (&v)[4])
+template <int OT>
+__device__ __forceinline__ void store1(const Mx4Product &p, size_t at, float v)
 {
-    const size_t at = (size_t)row * NO + n0;
-    if ((NO & 3) == 0) {
-        if (n0 >= NO) return;
-        if (p.otype == X_F32) {
-            *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
-        } else {
-            const bf16x2v a = {(__bf16)v[0], (__bf16)v[1]}, b = {(__bf16)v[2], (__bf16)v[3]};
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
-                make_uint2(__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b));
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (n0 + i < NO) store1(p, at + i, v[i]);
+    if (OT == X_F32) static_cast<float *>(p.out)[at] = v;
+    else static_cast<uint16_t *>(p.out)[at] = __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -291,30 +284,35 @@ __device__ __forceinline__ uint4 scales16(const uint8_t *row, int q, int n)
     }
     uint32_t h[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = 16 * q + 2 * i < n ? *reinterpret_cast<const uint16_t *>(row + 16 * q + 2 * i) : 0x7F7Fu;
+    for (int i = 0; i < 8; ++i) h[i] = *reinterpret_cast<const uint16_t *>(row + min(16 * q + 2 * i, n - 2));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = 16 * q + 2 * i < n ? h[i] : 0x7F7Fu;
     return make_uint4(h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16));
 }
 
+// Codes of columns past K: E2M1 zeros.
+__device__ const uint4 mx4_zeros = {0, 0, 0, 0};
+
 // MG: 32-row groups of the tile that hold rows.
-template <int MG>
+template <bool GLU, int OT, int MG>
 __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t, int nt, uint8_t *lds)
 {
     constexpr int MF = 2 * MG;           // 16-row fragments
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, li = lane & 15, lg = lane >> 4;
-    const bool glu = p.act == ACT_SWIGLU;
-    const int F = p.N >> 1, NO = glu ? F : p.N;
+    const int F = p.N >> 1, NO = GLU ? F : p.N;
     const int KB = p.K >> 1, KSC = p.K >> 5;              // bytes of codes, of scales per row
-    const int steps = (p.K + 127) >> 7;
-    const bool half = (p.K & 127) != 0;                   // the last step holds 64 columns
+    const int steps = (p.K + 127) >> 7;                   // the last one may hold 64 columns
 
     // weight row that row r of the block's 256 stands for: wave w's 64 rows are 32 gate and their 32
     // up rows with SwiGLU
     auto weight_row = [&](int r) {
         int n = nt * 256 + r;
-        if (glu) n = min(nt * 128 + (r >> 6) * 32 + (r & 31), F - 1) + ((r & 32) ? F : 0);
+        if (GLU) n = min(nt * 128 + (r >> 6) * 32 + (r & 31), F - 1) + ((r & 32) ? F : 0);
         return (size_t)t.g * p.N + min(n, p.N - 1);
     };
-    const bool live = (glu ? nt * 128 + wave * 32 : nt * 256 + wave * 64) < NO;
+    constexpr int WO = GLU ? 32 : 64;                     // a wave's outputs of a row
+    const int n0 = (nt * 4 + wave) * WO;
+    const bool live = n0 < NO;
 
     // ---- sources: 4 lanes read a row's 64 bytes; instruction i of a wave fills 16 rows.  Rows past the
     // tile's or the matrix's end read the last one, so that every wave issues the same loads.
@@ -333,9 +331,10 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
     uint8_t *xlds = lds + PB_WBUF * PB_WST, *slds = xlds + PB_XBUF * PB_XST;
     auto issue_w = [&](int s, int buf) {
         const uint32_t L = lds_addr(lds + buf * PB_WST);
-        const int off = min(min(s, steps - 1) * 64 + dchunk, KB - 16);
+        const int off = min(s, steps - 1) * 64 + dchunk;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) lds_dma16(wsrc[i] + off, L + (4 * wave + i) * 1024);
+        for (int i = 0; i < 4; ++i)
+            lds_dma16(off < KB ? wsrc[i] + off : reinterpret_cast<const uint8_t *>(&mx4_zeros), L + (4 * wave + i) * 1024);
     };
     auto issue_x = [&](int s) {
         const uint32_t L = lds_addr(xlds + (s & 1) * PB_XST);
@@ -355,7 +354,7 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
 #pragma unroll
         for (int f = 0; f < MF; ++f) acc[j][f] = zero4();
 
-    auto step = [&](int s, int buf, bool cut) {
+    auto step = [&](int s, int buf) {
         const uint8_t *X = xlds + (s & 1) * PB_XST, *W = lds + buf * PB_WST;
         const uint32_t *S = reinterpret_cast<const uint32_t *>(slds + ((s >> 2) & 1) * PB_SST) + (s & 3);
         const uint32_t *WS = S + 4 * (64 * wave + li), *XS = S + 4 * (PB_N + li);
@@ -364,9 +363,7 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
         int sa[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            uint4 v = *reinterpret_cast<const uint4 *>(W + wave * 4096 + chunk_at(16 * j + li, lg));
-            if (cut && lg >= 2) v = make_uint4(0, 0, 0, 0);    // columns past K
-            a[j] = code_reg(v);
+            a[j] = code_reg(*reinterpret_cast<const uint4 *>(W + wave * 4096 + chunk_at(16 * j + li, lg)));
             sa[j] = (int)(WS[64 * j] >> sh);
         }
 #pragma unroll
@@ -401,56 +398,81 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
         }
         if (s + 1 < steps) issue_x(s + 1);
         issue_w(s + 2, buf == 0 ? 2 : buf - 1);
-        if (live) step(s, buf, half && s + 1 == steps);
+        if (live) step(s, buf);
         if ((s & 3) == 3 && more) put_scales(q, sw, sx);
         buf = buf == 2 ? 0 : buf + 1;
     }
-    // no load may still be writing this block's LDS when it exits
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-
-    // ---- epilogue: lane l, element i of acc[j][f] is output 16 j + 4 (l / 16) + i of row 16 f + l % 16
+    // no load may still be writing LDS, and every wave is done reading it
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     if (!live) return;
+
+    // ---- epilogue: lane l, element i of acc[j][f] is output 16 j + 4 (l / 16) + i of row 16 f + l % 16.
+    // Each fragment's 16 rows turn round in the wave's own part of LDS, so that neighbouring lanes
+    // store neighbouring outputs of a row.
+    constexpr int RS = WO + 4, JN = GLU ? 2 : 4;
+    float *T = reinterpret_cast<float *>(lds) + wave * 16 * (64 + 4);
+    const bool whole = NO % (OT == X_F32 ? 4 : 8) == 0;
 #pragma unroll
     for (int f = 0; f < MF; ++f) {
-        const int r = 16 * f + li;
-        float v[4][4];
+        if (16 * f >= t.rows) break;
 #pragma unroll
-        for (int j = 0; j < (glu ? 2 : 4); ++j)
+        for (int j = 0; j < JN; ++j) {
+            f32x4 v;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[j][i] = glu ? silu_f32(acc[j][f][i]) * acc[j + 2 > 3 ? 3 : j + 2][f][i] : activate(acc[j][f][i], p.act);
-        const int nfr = glu ? 2 : 4, n0 = glu ? nt * 128 + wave * 32 : nt * 256 + wave * 64;
-        if (p.otype == X_MX4) {
-            // two fragments are one block of 32 outputs, spread over the four lanes of a row
+            for (int i = 0; i < 4; ++i) v[i] = GLU ? silu_fast(acc[j][f][i]) * acc[(j + 2) & 3][f][i] : activate(acc[j][f][i], p.act);
+            *reinterpret_cast<f32x4 *>(T + li * RS + 16 * j + 4 * lg) = v;
+        }
+        __builtin_amdgcn_wave_barrier();
+        const int r0 = t.row0 + 16 * f, rn = t.rows - 16 * f;
+        if (OT != X_MX4 && !whole) {
+#pragma unroll 1
+            for (int i = lane; i < 16 * WO; i += 64) {
+                const int r = i / WO, n = i & (WO - 1);
+                if (r < rn && n0 + n < NO) store1<OT>(p, (size_t)(r0 + r) * NO + n0 + n, T[r * RS + n]);
+            }
+        } else if (OT == X_F32) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (2 * b >= nfr) break;
+            for (int i = 0; i < 16 * WO / 4; i += 64) {
+                const int r = (i + lane) / (WO / 4), n = 4 * ((i + lane) & (WO / 4 - 1));
+                const f32x4 v = *reinterpret_cast<const f32x4 *>(T + r * RS + n);
+                if (r < rn && n0 + n < NO) *reinterpret_cast<f32x4 *>(static_cast<float *>(p.out) + (size_t)(r0 + r) * NO + n0 + n) = v;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16 * WO / 8; i += 64) {
+                const int r = (i + lane) / (WO / 8), n = 8 * ((i + lane) & (WO / 8 - 1));
                 float u[8];
-                uint32_t m = 0;
+                *reinterpret_cast<f32x4 *>(u) = *reinterpret_cast<const f32x4 *>(T + r * RS + n);
+                *reinterpret_cast<f32x4 *>(u + 4) = *reinterpret_cast<const f32x4 *>(T + r * RS + n + 4);
+                const bool in = r < rn && n0 + n < NO;
+                const size_t at = (size_t)(r0 + r) * NO + n0 + n;
+                if (OT == X_BF16) {
+                    typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+                    b8 o;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    u[i] = v[2 * b + (i >> 2)][i & 3];
-                    m = max(m, __float_as_uint(u[i]) & 0x7FFFFFFFu);
-                }
-                m = max(m, xor_lane_u32(m, 16, lane));
-                m = max(m, xor_lane_u32(m, 32, lane));
-                const uint32_t s = mx4_scale(m);
-                const uint32_t q = s == MX_NAN ? 0u : mx4_codes8(u, e8m0_f32(s));
-                const int nb = n0 + 32 * b;
-                if (r < t.rows && nb < NO) {
-                    uint8_t *o = static_cast<uint8_t *>(p.out) + (size_t)(t.row0 + r) * (NO >> 1) + (nb >> 1) + 2 * lg;
-                    *reinterpret_cast<uint16_t *>(o) = (uint16_t)q;
-                    *reinterpret_cast<uint16_t *>(o + 8) = (uint16_t)(q >> 16);
-                    if (lg == 0) p.out_scales[(size_t)(t.row0 + r) * (NO >> 5) + (nb >> 5)] = (uint8_t)s;
+                    for (int k = 0; k < 8; ++k) o[k] = (__bf16)u[k];
+                    if (in) *reinterpret_cast<b8 *>(static_cast<uint16_t *>(p.out) + at) = o;
+                } else {
+                    // four lanes hold a block of 32 outputs
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(u[k]) & 0x7FFFFFFFu);
+                    m = max(m, dpp_u32<0xB1>(m));
+                    m = max(m, dpp_u32<0x4E>(m));
+                    const uint32_t sc = mx4_scale(m);
+                    const uint32_t q = sc == MX_NAN ? 0u : mx4_codes8(u, e8m0_f32(sc));
+                    if (in) {
+                        reinterpret_cast<uint32_t *>(p.out)[at >> 3] = q;
+                        if ((lane & 3) == 0) p.out_scales[at >> 5] = (uint8_t)sc;
+                    }
                 }
             }
-        } else if (r < t.rows) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (j < nfr) store4(p, t.row0 + r, n0 + 16 * j + 4 * lg, NO, v[j]);
         }
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
+template <bool GLU, int OT>
 __global__ __launch_bounds__(256, 2) void product_mx4_kernel(Mx4Product p, int ntiles)
 {
     __shared__ __attribute__((aligned(16))) uint8_t mx4_lds[PB_LDS];
@@ -458,10 +480,10 @@ __global__ __launch_bounds__(256, 2) void product_mx4_kernel(Mx4Product p, int n
     const Tile t = find_tile(p, blockIdx.x, PB_M, ntiles, threadIdx.x & 63, nt);
     if (t.rows < 1) return;
     switch ((t.rows + 31) >> 5) {
-    case 1: product_tile<1>(p, t, nt, mx4_lds); break;
-    case 2: product_tile<2>(p, t, nt, mx4_lds); break;
-    case 3: product_tile<3>(p, t, nt, mx4_lds); break;
-    default: product_tile<4>(p, t, nt, mx4_lds); break;
+    case 1: product_tile<GLU, OT, 1>(p, t, nt, mx4_lds); break;
+    case 2: product_tile<GLU, OT, 2>(p, t, nt, mx4_lds); break;
+    case 3: product_tile<GLU, OT, 3>(p, t, nt, mx4_lds); break;
+    default: product_tile<GLU, OT, 4>(p, t, nt, mx4_lds); break;
     }
 }
 
@@ -641,7 +663,7 @@ __global__ __launch_bounds__(64 * NW) void product_wide_kernel(Mx4Product p, int
                         if (glu) u += red[k][at + (TN / 2) * 256];
                     }
                     if (n0 + n < NO)
-                        store1(p, (size_t)(t.row0 + r0 + 16 * m + r) * NO + n0 + n, glu ? silu_f32(v) * u : activate(v, p.act));
+                        (p.otype == X_F32 ? store1<X_F32> : store1<X_BF16>)(p, (size_t)(t.row0 + r0 + 16 * m + r) * NO + n0 + n, glu ? silu_f32(v) * u : activate(v, p.act));
                 }
             }
         }
@@ -703,7 +725,16 @@ hipError_t launch_product_mx4(const Mx4Product &p, hipStream_t s)
     const int ntiles = (NO + per - 1) / per;
     const int rows = p.Pr + p.S * p.T, G = p.offsets ? p.E + p.S : 1;
     const int mtiles = rows / PB_M + (rows < G ? rows : G);        // at least the sum of the groups' tiles
-    product_mx4_kernel<<<((unsigned)mtiles * ntiles + 7) / 8 * 8, 256, 0, s>>>(p, ntiles);
+    const unsigned grid = ((unsigned)mtiles * ntiles + 7) / 8 * 8;
+    const bool glu = p.act == ACT_SWIGLU;
+    auto go = [&](auto g, auto o) { product_mx4_kernel<g.value, o.value><<<grid, 256, 0, s>>>(p, ntiles); };
+    auto by_out = [&](auto g) {
+        if (p.otype == X_F32) go(g, std::integral_constant<int, X_F32>{});
+        else if (p.otype == X_BF16) go(g, std::integral_constant<int, X_BF16>{});
+        else go(g, std::integral_constant<int, X_MX4>{});
+    };
+    if (glu) by_out(std::true_type{});
+    else by_out(std::false_type{});
     return hipGetLastError();
 }
 
