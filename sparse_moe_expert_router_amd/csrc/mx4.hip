@@ -234,6 +234,27 @@ __device__ __forceinline__ void store1(const Mx4Product &p, size_t at, float v)
     else static_cast<uint16_t *>(p.out)[at] = __builtin_bit_cast(uint16_t, (__bf16)v);
 }
 
+// four consecutive outputs from column n on, at element `at`; those below NO exist
+__device__ __forceinline__ void store4(const Mx4Product &p, size_t at, int n, int NO, const float (&v)[4])
+{
+    if (NO & 3) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (n + i < NO) {
+                if (p.otype == X_F32) store1<X_F32>(p, at + i, v[i]);
+                else store1<X_BF16>(p, at + i, v[i]);
+            }
+    } else if (n < NO) {
+        if (p.otype == X_F32) {
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) = make_float4(v[0], v[1], v[2], v[3]);
+        } else {
+            typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+            const b4 o = {(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+            *reinterpret_cast<b4 *>(static_cast<uint16_t *>(p.out) + at) = o;
+        }
+    }
+}
+
 // ---------------------------------------------------------------------------------------------
 // Product of MX4 rows.  A block of 4 waves computes BM = 128 rows by BN = 256 weight rows (128 gate
 // rows and their 128 up rows with SwiGLU); wave w owns 64 of the weight rows and all 128 rows.
@@ -488,10 +509,14 @@ __global__ __launch_bounds__(256, 2) void product_mx4_kernel(Mx4Product p, int n
 }
 
 // ---------------------------------------------------------------------------------------------
-// Product of bf16 / fp32 rows with MX4 weights.  A block owns TN 16-row weight tiles (with SwiGLU
-// TN / 2 gate tiles and their up tiles) of one group; its waves split K and the partial sums meet
-// in LDS in wave order.  Weights widen to bf16 exactly; an fp32 x is cut into three bf16 terms
-// whose sum is x, so every product is exact and the sums are fp32.
+// Product of bf16 / fp32 rows with MX4 weights: few rows per group, so streaming the weights is what
+// counts.  A wave owns sets of 64 weight rows (with SwiGLU 32 gate rows and their up rows), or with
+// KS > 1 every KS-th step of 128 columns of a set, and streams their codes and scales through a ring
+// of its own in LDS by direct-to-LDS loads (neighbouring lanes read neighbouring bytes; straight into
+// the matrix cores' lanes every lane would be a cache access of its own).  Only its own loads fill
+// the ring, so it runs without barriers.  The group's rows of x lie in LDS for all sets and waves of
+// the block, as bf16: an fp32 x is cut into three terms whose sum is x, weights widen exactly, so
+// every product is exact and the sums are fp32.
 
 template <int XK>
 struct XTerms {
@@ -520,172 +545,239 @@ __device__ __forceinline__ void cut_f32x8(const float *v, bf16x8 (&terms)[3])
     terms[2] = c.v;
 }
 
-// A block takes `iters` such sets of weight tiles, one after another.  A wave's share of K runs in
-// batches of U steps of 128 columns; a batch's weights and scales are asked for while the batch
-// before it (of the same tiles or of the set before) is multiplied, so TN x U KB are in flight per
-// wave all the time.
-template <int XK, int TN, int MT, int NW, int U>
-__global__ __launch_bounds__(64 * NW) void product_wide_kernel(Mx4Product p, int iters)
+constexpr int PW_WAVES = 4, PW_RING = 3;               // waves of a block, stages of a wave's ring
+constexpr int PW_STAGE = 64 * 64 + 2 * 64 * 4;         // codes, then scales (two dwords per row) of 128 columns
+constexpr int PW_LOADS = 6;                            // load instructions of a stage
+constexpr int PW_SLAB = 24 * 1024;                     // x
+
+// 2 bytes per lane, each zero-extended into the dword lds + 4 l of lane l.
+__device__ __forceinline__ void lds_dma2(const void *g, uint32_t lds)
 {
-    constexpr int NTERM = XTerms<XK>::N, XB = XK == X_F32 ? 4 : 2;
-    __shared__ float red[NW][TN * 256];
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, off"
+                 :: "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(g) : "memory", "m0");
+}
+
+// MT: 16-row fragments of x at a time.
+template <int XK, bool GLU, int MT, int KS>
+__global__ __launch_bounds__(64 * PW_WAVES, 2) void product_wide_kernel(Mx4Product p, int iters)
+{
+    constexpr int NTERM = XTerms<XK>::N, SETS = PW_WAVES / KS;
+    __shared__ __attribute__((aligned(16))) uint8_t s_ring[PW_WAVES * PW_RING * PW_STAGE];
+    __shared__ __attribute__((aligned(16))) uint8_t s_slab[PW_SLAB];
+    __shared__ int s_src[16 * MT];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, li = lane & 15, lg = lane >> 4;
     const Tile t = find_slot(p, blockIdx.y, lane);
     if (t.rows < 1) return;
-    const bool glu = p.act == ACT_SWIGLU;
-    const int F = p.N >> 1, NO = glu ? F : p.N;
-    const int TO = glu ? TN / 2 : TN;                      // output tiles
+    constexpr int WO = GLU ? 32 : 64;                      // outputs of a set
+    const int F = p.N >> 1, NO = GLU ? F : p.N;
     const int KB = p.K >> 1, KSC = p.K >> 5, steps = (p.K + 127) >> 7;
-    const int per = (steps + NW - 1) / NW, s0 = wave * per, s1 = min(steps, s0 + per);
-    const int nbatch = (per + U - 1) / U;                  // the same in every wave
-    const int nset0 = blockIdx.x * iters, nsets = min(iters, (NO + 16 * TO - 1) / (16 * TO) - nset0);
+    const int ks = wave % KS, set0 = blockIdx.x * iters * SETS + wave / KS;
+    const int nsets = (NO + WO - 1) / WO;
+    uint8_t *ring = s_ring + wave * PW_RING * PW_STAGE;
+    const int drow = lane >> 2, dchunk = 16 * ((lane & 3) ^ ((lane >> 4) & 3));
 
-    struct Batch {
-        uint4 w[U][TN];
-        uint32_t s[U][TN];
-    };
-    auto load = [&](Batch &b, int it, int ib) {
-        const int n0 = (nset0 + it) * TO * 16;
+    // this wave's sets, set0, set0 + SETS, ..: how many of the block's turns it has
+    const int turns = min(iters, max(0, (nsets - set0 + SETS - 1) / SETS));
+    // rows at a time: as many as KS steps of x fit the slab for
+    constexpr int RM = PW_SLAB / (2 * NTERM * (KS * 128 + 8)) < 16 * MT ? PW_SLAB / (2 * NTERM * (KS * 128 + 8)) : 16 * MT;
+
+    for (int r0 = 0; r0 < t.rows; r0 += RM) {
+        const int R = min(RM, t.rows - r0);
+        // ---- the wave's stream of stages: steps ks, ks + KS, .. of set 0, then of set 1, ..
+        int it_p = 0, s_p = ks, buf_p = 0;
+        const uint8_t *wsrc[4], *wsc;
+        auto open_set = [&](int it) {
+            const int n0 = (set0 + it * SETS) * WO;
+            auto weight_row = [&](int r) {
+                int n = n0 + r;
+                if (GLU) n = min(n0 + (r & 31), F - 1) + ((r & 32) ? F : 0);
+                return (size_t)t.g * p.N + min(n, p.N - 1);
+            };
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            int n;
-            if (glu) {
-                const int f = min(n0 + 16 * (j % (TN / 2)) + li, F - 1);
-                n = j < TN / 2 ? f : F + f;
-            } else {
-                n = min(n0 + 16 * j + li, p.N - 1);
+            for (int i = 0; i < 4; ++i) wsrc[i] = p.w + weight_row(16 * i + drow) * KB;
+            wsc = p.ws + weight_row(lane) * KSC;
+        };
+        // Every call issues PW_LOADS loads, past the stream's end the last step's again, so that the
+        // count of loads in flight holds.
+        auto issue = [&] {
+            const uint32_t L = lds_addr(ring + buf_p * PW_STAGE);
+            const int s = min(s_p, steps - 1), off = s * 64 + dchunk;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                lds_dma16(off < KB ? wsrc[i] + off : reinterpret_cast<const uint8_t *>(&mx4_zeros), L + i * 1024);
+            lds_dma2(wsc + 4 * s, L + 4096);
+            // the last step's missing blocks take the present ones' scales (their codes are zeros)
+            lds_dma2(wsc + (4 * s + 2 < KSC ? 4 * s + 2 : 4 * s), L + 4096 + 256);
+            buf_p = buf_p == PW_RING - 1 ? 0 : buf_p + 1;
+            s_p += KS;
+            if (s_p >= steps && it_p + 1 < turns) {
+                s_p = ks;
+                open_set(++it_p);
             }
-            const size_t row = (size_t)t.g * p.N + n;
-            const uint8_t *wp = p.w + row * KB + 16 * lg, *sp = p.ws + row * KSC + lg;
+        };
+        if (turns > 0) {
+            open_set(0);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int s = s0 + ib * U + u;
-                b.w[u][j] = make_uint4(0, 0, 0, 0);
-                b.s[u][j] = 127;
-                if (s < s1 && 128 * s + 32 * lg < p.K) {
-                    b.w[u][j] = *reinterpret_cast<const uint4 *>(wp + (size_t)s * 64);
-                    b.s[u][j] = sp[s * 4];
+            for (int i = 0; i < PW_RING - 1; ++i) issue();
+        }
+
+        // ---- x: [term][row][columns of a slab + 8]; the slab holds all of K where it fits
+        if (tid < R) s_src[tid] = source_row(p, t.row0 + r0 + tid);
+        const int SC = (PW_SLAB / (2 * NTERM * R) - 8) / 128 / KS * KS;   // steps of a slab, at least KS
+        const int XS = min(SC, steps) * 128 + 8;                   // bf16 values of a slab row
+        const int nslab = (steps + SC - 1) / SC;
+        uint16_t *slab = reinterpret_cast<uint16_t *>(s_slab);
+        auto load_slab = [&](int b) {
+            const int c0 = b * SC * 128, pieces = (min(steps, (b + 1) * SC) * 128 - c0) / 8;
+            for (int i = tid; i < R * pieces; i += 64 * PW_WAVES) {
+                const int r = i / pieces, c = 8 * (i - r * pieces);
+                const size_t at = (size_t)s_src[r] * p.K + c0 + c;
+                const bool in = c0 + c < p.K;
+                uint16_t *dst = slab + r * XS + c;
+                if constexpr (XK == X_F32) {
+                    float v[8] = {};
+                    if (in) {
+                        const float4 *g = reinterpret_cast<const float4 *>(static_cast<const float *>(p.x) + at);
+                        const float4 a = g[0], b4 = g[1];
+                        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+                        v[4] = b4.x; v[5] = b4.y; v[6] = b4.z; v[7] = b4.w;
+                    }
+                    bf16x8 xt[3];
+                    cut_f32x8(v, xt);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) *reinterpret_cast<bf16x8 *>(dst + k * R * XS) = xt[k];
+                } else {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (in) v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + at);
+                    *reinterpret_cast<uint4 *>(dst) = v;
                 }
             }
-        }
-    };
+        };
 
-    for (int r0 = 0; r0 < t.rows; r0 += 16 * MT) {
-        const uint8_t *xp[MT];
-        bool in[MT];
-        Batch next;
-        load(next, 0, 0);
+        int buf = 0;
+        for (int it = 0; it < iters; ++it) {
+            f32x4 acc[4][MT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const int r = r0 + 16 * m + li;
-            in[m] = r < t.rows;
-            const size_t src = source_row(p, t.row0 + min(r, t.rows - 1));
-            xp[m] = static_cast<const uint8_t *>(p.x) + (src * p.K + 32 * lg) * XB;
-        }
-        for (int it = 0; it < nsets; ++it) {
-            f32x4 acc[TN][MT];
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+                for (int m = 0; m < MT; ++m) acc[j][m] = zero4();
+            for (int b = 0; b < nslab; ++b) {
+                if (nslab > 1 || it == 0) {
+                    lds_barrier();
+                    load_slab(b);
+                    lds_barrier();
+                }
+                const int send = it < turns ? min(steps, (b + 1) * SC) : 0;
+                for (int s = b * SC + ks; s < send; s += KS) {
+                    // this stage has landed, and what was read from the next buffer to fill has arrived
+                    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(PW_LOADS * (PW_RING - 2)) : "memory");
+                    issue();
+                    const uint8_t *W = ring + buf * PW_STAGE;
+                    const uint32_t *S = reinterpret_cast<const uint32_t *>(W + 4096) + (lg >> 1) * 64 + li;
+                    buf = buf == PW_RING - 1 ? 0 : buf + 1;
+                    uint4 w[4];
+                    float sc[4];
 #pragma unroll
-                for (int j = 0; j < TN; ++j) acc[j][m] = zero4();
-            for (int ib = 0; ib < nbatch; ++ib) {
-                const Batch cur = next;
-                const bool last = ib + 1 == nbatch;
-                if (!last || it + 1 < nsets) load(next, last ? it + 1 : it, last ? 0 : ib + 1);
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int s = s0 + ib * U + u;
-                    if (s >= s1) break;
-                    const bool kin = 128 * s + 32 * lg < p.K;
-                    float sc[TN];
-#pragma unroll
-                    for (int j = 0; j < TN; ++j) sc[j] = e8m0_f32(cur.s[u][j]);
+                    for (int j = 0; j < 4; ++j) {
+                        w[j] = *reinterpret_cast<const uint4 *>(W + chunk_at(16 * j + li, lg));
+                        sc[j] = e8m0_f32((S[16 * j] >> (8 * (lg & 1))) & 0xFFu);
+                    }
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
-                        if (MT > 1 && r0 + 16 * m >= t.rows) break;
-                        bf16x8 xt[4][NTERM];
-                        if constexpr (XK == X_F32) {
-                            float v[4][8] = {};
-                            if (in[m] && kin) {
+                        if (MT > 1 && 16 * m >= R) break;
+                        const uint16_t *X = slab + min(16 * m + li, R - 1) * XS + (s - b * SC) * 128 + 32 * lg;
 #pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    const float4 *g = reinterpret_cast<const float4 *>(xp[m] + ((size_t)s * 128 + 8 * q) * 4);
-                                    const float4 a = g[0], b = g[1];
-                                    v[q][0] = a.x; v[q][1] = a.y; v[q][2] = a.z; v[q][3] = a.w;
-                                    v[q][4] = b.x; v[q][5] = b.y; v[q][6] = b.z; v[q][7] = b.w;
-                                }
-                            }
+                        for (int q = 0; q < 4; ++q) {
+                            bf16x8 xt[NTERM];
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) cut_f32x8(v[q], xt[q]);
-                        } else {
-                            U4 v[4];
+                            for (int k = 0; k < NTERM; ++k) xt[k] = *reinterpret_cast<const bf16x8 *>(X + k * R * XS + 8 * q);
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) v[q].u = make_uint4(0, 0, 0, 0);
-                            if (in[m] && kin) {
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    v[q].u = *reinterpret_cast<const uint4 *>(xp[m] + ((size_t)s * 128 + 8 * q) * 2);
-                            }
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) xt[q][0] = v[q].v;
-                        }
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-#pragma unroll
-                            for (int j = 0; j < TN; ++j) {
-                                const uint4 &wj = cur.w[u][j];
-                                const uint32_t c = q == 0 ? wj.x : q == 1 ? wj.y : q == 2 ? wj.z : wj.w;
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t c = q == 0 ? w[j].x : q == 1 ? w[j].y : q == 2 ? w[j].z : w[j].w;
                                 const bf16x8 wb = mx4_bf16x8(c, sc[j]);
 #pragma unroll
-                                for (int k = NTERM - 1; k >= 0; --k) acc[j][m] = mfma16x16x32_bf16(wb, xt[q][k], acc[j][m]);
+                                for (int k = NTERM - 1; k >= 0; --k) acc[j][m] = mfma16x16x32_bf16(wb, xt[k], acc[j][m]);
                             }
+                        }
                     }
                 }
             }
-            // ---- the waves' sums, then the activation; element i of a lane is weight row 4 lg + i of x row li
-            const int n0 = (nset0 + it) * TO * 16;
+            if (it >= turns) continue;
+            // ---- element i of a lane's acc[j][m] is weight row 16 j + 4 lg + i of x row 16 m + li
+            const int n0 = (set0 + it * SETS) * WO;
+            if constexpr (KS > 1) {
+                // the KS waves' sums meet in LDS, in wave order (iters is 1: the rings are idle)
+                float *red = reinterpret_cast<float *>(ring);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (r0 + 16 * m >= t.rows) break;
-                if (m > 0 || it > 0 || r0 > 0) lds_barrier();
+                for (int m = 0; m < MT; ++m) {
+                    if (16 * m >= R) break;
+                    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    *reinterpret_cast<f32x4 *>(&red[wave][j * 256 + li * 16 + 4 * lg]) = acc[j][m];
-                lds_barrier();
-                const int rows = min(16, t.rows - r0 - 16 * m);
-                for (int i = tid; i < rows * 16 * TO; i += 64 * NW) {
-                    const int r = i / (16 * TO), n = i - r * 16 * TO;
-                    const int at = (n >> 4) * 256 + r * 16 + (n & 15);
-                    float v = 0.f, u = 0.f;
+                    for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4 *>(red + li * 68 + 16 * j + 4 * lg) = acc[j][m];
+                    lds_barrier();
+                    const int rows = min(16, R - 16 * m);
+                    for (int i = ks * 64 + lane; i < rows * WO; i += KS * 64) {
+                        const int r = i / WO, n = i & (WO - 1);
+                        const float *q = reinterpret_cast<const float *>(s_ring + (wave - ks) * PW_RING * PW_STAGE) + r * 68 + n;
+                        float v = 0.f, u = 0.f;
 #pragma unroll
-                    for (int k = 0; k < NW; ++k) {
-                        v += red[k][at];
-                        if (glu) u += red[k][at + (TN / 2) * 256];
+                        for (int k = 0; k < KS; ++k) {
+                            v += q[k * (PW_RING * PW_STAGE / 4)];
+                            if (GLU) u += q[k * (PW_RING * PW_STAGE / 4) + 32];
+                        }
+                        if (n0 + n < NO) {
+                            v = GLU ? silu_fast(v) * u : activate(v, p.act);
+                            const size_t at = (size_t)(t.row0 + r0 + 16 * m + r) * NO + n0 + n;
+                            if (p.otype == X_F32) store1<X_F32>(p, at, v);
+                            else store1<X_BF16>(p, at, v);
+                        }
                     }
-                    if (n0 + n < NO)
-                        (p.otype == X_F32 ? store1<X_F32> : store1<X_BF16>)(p, (size_t)(t.row0 + r0 + 16 * m + r) * NO + n0 + n, glu ? silu_f32(v) * u : activate(v, p.act));
+                }
+            } else {
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+                    if (16 * m + li >= R) continue;
+                    const size_t row = (size_t)(t.row0 + r0 + 16 * m + li) * NO;
+#pragma unroll
+                    for (int j = 0; j < (GLU ? 2 : 4); ++j) {
+                        const int n = n0 + 16 * j + 4 * lg;
+                        float v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            v[i] = GLU ? silu_fast(acc[j][m][i]) * acc[(j + 2) & 3][m][i] : activate(acc[j][m][i], p.act);
+                        store4(p, row + n, n, NO, v);
+                    }
                 }
             }
         }
+        // no load may still be writing LDS
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     }
 }
 
-template <int XK, int TN, int NW, int U>
+template <int XK, bool GLU, int KS>
+hipError_t launch_wide(const Mx4Product &p, int iters, const dim3 &grid, bool many, hipStream_t s)
+{
+    if (many) product_wide_kernel<XK, GLU, XK == X_F32 ? 2 : 4, KS><<<grid, 64 * PW_WAVES, 0, s>>>(p, iters);
+    else product_wide_kernel<XK, GLU, 1, KS><<<grid, 64 * PW_WAVES, 0, s>>>(p, iters);
+    return hipGetLastError();
+}
+
+template <int XK, bool GLU>
 hipError_t launch_wide(const Mx4Product &p, hipStream_t s)
 {
-    const int TO = p.act == ACT_SWIGLU ? TN / 2 : TN;
-    const int NO = p.act == ACT_SWIGLU ? p.N / 2 : p.N;
-    const int rows = p.Pr + p.S * p.T;
-    const int G = p.offsets ? p.E + p.S : 1;
-    const int slots = rows < G ? rows : G, sets = (NO + 16 * TO - 1) / (16 * TO);
-    static const int BL = getenv("WB") ? atoi(getenv("WB")) : 2048;
-    int iters = (int)((long long)sets * slots / BL);
-    iters = iters < 1 ? 1 : (iters > sets ? sets : iters);
-    const dim3 grid((sets + iters - 1) / iters, slots);
+    const int WO = GLU ? 32 : 64, NO = GLU ? p.N / 2 : p.N;
+    const int rows = p.Pr + p.S * p.T, G = p.offsets ? p.E + p.S : 1;
+    const int slots = rows < G ? rows : G, sets = (NO + WO - 1) / WO;
+    static const int vk = getenv("WK") ? atoi(getenv("WK")) : 0, vi = getenv("WI") ? atoi(getenv("WI")) : 0;
+    int KS = 1, iters = 1;
+    if (vk) KS = vk;
+    if (vi && KS == 1) iters = vi;
+    const int per = PW_WAVES / KS * iters;
+    const dim3 grid((sets + per - 1) / per, slots);
     // 16 rows at a time where groups hold few, 64 where they hold many
-    if (rows <= 16 || rows < 8 * G) product_wide_kernel<XK, TN, 1, NW, U><<<grid, 64 * NW, 0, s>>>(p, iters);
-    else product_wide_kernel<XK, TN, 4, NW, U><<<grid, 64 * NW, 0, s>>>(p, iters);
-    return hipGetLastError();
+    const bool many = rows > 16 && rows >= 8 * G;
+    return KS == 1 ? launch_wide<XK, GLU, 1>(p, iters, grid, many, s) : launch_wide<XK, GLU, 4>(p, 1, grid, many, s);
 }
 
 }  // namespace
@@ -715,10 +807,9 @@ hipError_t launch_product_mx4(const Mx4Product &p, hipStream_t s)
 {
     ProfScope prof(K_PRODUCT_MX4, s);
     if (p.xtype != X_MX4) {
-        static const int var = getenv("WV") ? atoi(getenv("WV")) : 0;
-#define V(i, TN, NW, U) if (var == i) return p.xtype == X_F32 ? launch_wide<X_F32, TN, NW, U>(p, s) : launch_wide<X_BF16, TN, NW, U>(p, s);
-        V(0, 4, 4, 2) V(1, 4, 8, 1) V(2, 4, 4, 1) V(3, 8, 4, 1) V(4, 4, 2, 2) V(5, 8, 2, 1) V(6, 8, 8, 1) V(7, 4, 1, 2)
-#undef V
+        const bool g = p.act == ACT_SWIGLU;
+        if (p.xtype == X_F32) return g ? launch_wide<X_F32, true>(p, s) : launch_wide<X_F32, false>(p, s);
+        return g ? launch_wide<X_BF16, true>(p, s) : launch_wide<X_BF16, false>(p, s);
     }
     const int NO = p.act == ACT_SWIGLU ? p.N / 2 : p.N;
     const int per = p.act == ACT_SWIGLU ? PB_N / 2 : PB_N;
