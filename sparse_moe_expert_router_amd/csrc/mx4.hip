@@ -9,7 +9,6 @@
 //    rows per group, where streaming the weights is all that counts.
 #include <hip/hip_runtime.h>
 
-#include <cstdlib>
 #include <type_traits>
 
 #include "moe_launch.hpp"
@@ -81,55 +80,89 @@ __global__ __launch_bounds__(256) void quantize_mx4_kernel(const XT *__restrict_
 }
 
 // ---------------------------------------------------------------------------------------------
-// Groups.  The offsets live on the device, so a block finds its rows itself: one wave holds the
-// groups' row counts, 64 per register, and scans them.
+// Groups.  The offsets live on the device, so every wave finds its block's rows itself: lane l holds
+// groups 8 l .. 8 l + 7, which three loads fetch, and one scan over the lanes numbers the tiles.  The
+// S shared groups follow the E routed ones and need no loads.
 
 struct Tile {
     int g, row0, rows;      // group, first row, rows (0: no such tile)
 };
 
-__device__ __forceinline__ int wave_scan_incl(int v, int lane)
+constexpr int GPL = 8;      // groups per lane
+static_assert(GPL * WAVE >= MAX_E, "a wave holds every group");
+
+// Offsets are clamped into [0, Pr] and taken as ascending, so no value of theirs leads outside the rows.
+__device__ __forceinline__ void load_groups(const Mx4Product &p, int lane, int (&lo)[GPL], int (&hi)[GPL])
 {
+    const int g0 = GPL * lane;
+    int o[GPL + 1] = {};
+    if (g0 + GPL <= p.E) {
+        const int4 a = *reinterpret_cast<const int4 *>(p.offsets + g0), b = *reinterpret_cast<const int4 *>(p.offsets + g0 + 4);
+        o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+        o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+        o[8] = p.offsets[g0 + 8];
+    } else if (g0 < p.E) {
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const int t = __shfl_up(v, o, WAVE);
-        v += lane >= o ? t : 0;
+        for (int i = 0; i <= GPL; ++i) o[i] = p.offsets[min(g0 + i, p.E)];
     }
+#pragma unroll
+    for (int i = 0; i < GPL; ++i) {
+        lo[i] = min(max(o[i], 0), p.Pr);
+        hi[i] = min(max(o[i + 1], lo[i]), p.Pr);
+    }
+}
+
+// inclusive sum over the lanes up to this one
+__device__ __forceinline__ int wave_scan_incl(int v)
+{
+    // within rows of 16 lanes by DPP row shifts, then the rows' ends onto the rows behind them
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);
     return v;
 }
 
-// The groups' rows, 64 groups per register, their loads all in flight together.  Offsets are clamped
-// into [0, Pr] and taken as ascending, so no value of theirs leads outside the rows.
-constexpr int GROUP_REGS = (MAX_E + MAX_SHARED + 63) / 64;
-struct Groups {
-    int lo[GROUP_REGS], hi[GROUP_REGS];
-};
-__device__ __forceinline__ Groups load_groups(const Mx4Product &p, int lane)
-{
-    Groups q;
-    const int G = p.E + p.S;
+// The tiles of all groups when each group's rows are cut into tiles of `bm`: their number, and tile
+// `tile` (a negative one: none).
+struct Tiling {
+    int lo[GPL], hi[GPL], nt, incl, routed, total;
+    __device__ __forceinline__ Tiling(const Mx4Product &p, int bm, int lane)
+    {
+        load_groups(p, lane, lo, hi);
+        nt = 0;
 #pragma unroll
-    for (int c = 0; c < GROUP_REGS; ++c) {
-        const int g = 64 * c + lane;
-        q.lo[c] = q.hi[c] = 0;
-        if (64 * c < G) {
-            if (g < p.E) {
-                q.lo[c] = p.offsets[g];
-                q.hi[c] = p.offsets[g + 1];
-            } else if (g < G) {
-                q.lo[c] = p.Pr + (g - p.E) * p.T;
-                q.hi[c] = q.lo[c] + p.T;
-            }
-        }
+        for (int i = 0; i < GPL; ++i) nt += (hi[i] - lo[i] + bm - 1) / bm;
+        incl = wave_scan_incl(nt);
+        routed = __builtin_amdgcn_readlane(incl, 63);
+        total = routed + p.S * ((p.T + bm - 1) / bm);
     }
-#pragma unroll
-    for (int c = 0; c < GROUP_REGS; ++c)
-        if (64 * c + lane < p.E) {
-            q.lo[c] = min(max(q.lo[c], 0), p.Pr);
-            q.hi[c] = min(max(q.hi[c], q.lo[c]), p.Pr);
+    __device__ __forceinline__ Tile find(const Mx4Product &p, int bm, int tile) const
+    {
+        if (tile < 0 || tile >= total) return Tile{0, 0, 0};
+        if (tile >= routed) {
+            const int per = (p.T + bm - 1) / bm, s = (tile - routed) / per, r = (tile - routed - s * per) * bm;
+            return Tile{p.E + s, p.Pr + s * p.T + r, min(bm, p.T - r)};
         }
-    return q;
-}
+        const int at = __ffsll((long long)__ballot(incl > tile)) - 1;      // the lane that holds it
+        int left = tile - __builtin_amdgcn_readlane(incl - nt, at), g = 0, l = 0, h = 0;
+        bool open = true;
+#pragma unroll
+        for (int i = 0; i < GPL; ++i) {
+            const int a = __builtin_amdgcn_readlane(lo[i], at), b = __builtin_amdgcn_readlane(hi[i], at), n = (b - a + bm - 1) / bm;
+            if (open && left < n) {
+                g = i;
+                l = a;
+                h = b;
+                open = false;
+            }
+            if (open) left -= n;
+        }
+        return Tile{GPL * at + g, l + left * bm, min(bm, h - l - left * bm)};
+    }
+};
 
 // Block b's tile when every group's rows are cut into tiles of `bm` and the weight rows into
 // `ntiles`.  Blocks go to the 8 XCDs in turn, so each XCD takes a contiguous eighth of the tiles,
@@ -137,70 +170,27 @@ __device__ __forceinline__ Groups load_groups(const Mx4Product &p, int lane)
 // weight tiles of one row tile, which read the same rows, meet in one L2.
 __device__ __forceinline__ Tile find_tile(const Mx4Product &p, int b, int bm, int ntiles, int lane, int &nt)
 {
-    const int G = p.E + p.S;
-    Groups q;
-    int incl[GROUP_REGS], before[GROUP_REGS], total = 0;
+    const auto mine = [&](int total) {
+        const long long live = (long long)total * ntiles;
+        const int x = b & 7, j0 = (int)(live * x / 8), j = j0 + (b >> 3);
+        const bool in = j < (int)(live * (x + 1) / 8);
+        const int tile = j / ntiles;
+        nt = j - tile * ntiles;
+        return in ? tile : -1;
+    };
     if (p.offsets == nullptr) {
-        total = (p.Pr + bm - 1) / bm;
-    } else {
-        q = load_groups(p, lane);
-#pragma unroll
-        for (int c = 0; c < GROUP_REGS; ++c)
-            if (64 * c < G) incl[c] = wave_scan_incl((q.hi[c] - q.lo[c] + bm - 1) / bm, lane);
-#pragma unroll
-        for (int c = 0; c < GROUP_REGS; ++c) {
-            before[c] = total;
-            if (64 * c < G) total += __builtin_amdgcn_readlane(incl[c], 63);
-        }
+        const int tile = mine((p.Pr + bm - 1) / bm);
+        return tile < 0 ? Tile{0, 0, 0} : Tile{0, tile * bm, min(bm, p.Pr - tile * bm)};
     }
-    const int live = total * ntiles, x = b & 7, i = b >> 3;
-    const int j0 = (int)((long long)live * x / 8), j1 = (int)((long long)live * (x + 1) / 8);
-    Tile t{0, 0, 0};
-    nt = 0;
-    if (j0 + i >= j1) return t;
-    const int tile = (j0 + i) / ntiles;
-    nt = j0 + i - tile * ntiles;
-    if (p.offsets == nullptr) return Tile{0, tile * bm, min(bm, p.Pr - tile * bm)};
-#pragma unroll
-    for (int c = 0; c < GROUP_REGS; ++c) {
-        if (64 * c >= G) continue;
-        const unsigned long long m = __ballot(before[c] + incl[c] > tile);
-        if (m && before[c] <= tile) {
-            const int at = __ffsll((long long)m) - 1;
-            const int lo = __builtin_amdgcn_readlane(q.lo[c], at), hi = __builtin_amdgcn_readlane(q.hi[c], at);
-            const int first = before[c] + __builtin_amdgcn_readlane(incl[c], at) - (hi - lo + bm - 1) / bm;
-            const int r0 = lo + (tile - first) * bm;
-            t = Tile{64 * c + at, r0, min(bm, hi - r0)};
-            break;
-        }
-    }
-    return t;
+    const Tiling q(p, bm, lane);
+    return q.find(p, bm, mine(q.total));
 }
 
-// The `slot`-th group that holds rows, all of its rows.  A group holds rows or not, so a ballot and
-// bit counts find it; the loads of all groups' offsets go out together.
+// The `slot`-th group that holds rows, all of its rows (a tile of 2^30 rows holds any group).
 __device__ __forceinline__ Tile find_slot(const Mx4Product &p, int slot, int lane)
 {
     if (p.offsets == nullptr) return Tile{0, 0, slot == 0 ? p.Pr : 0};
-    const int G = p.E + p.S;
-    const Groups q = load_groups(p, lane);
-    Tile t{0, 0, 0};
-    int before = 0;
-#pragma unroll
-    for (int c = 0; c < GROUP_REGS; ++c) {
-        if (64 * c >= G) continue;
-        const unsigned long long m = __ballot(q.hi[c] > q.lo[c]);
-        const int n = __popcll(m);
-        if (slot >= before && slot < before + n) {
-            const unsigned long long below = (1ull << lane) - 1;
-            const unsigned long long at = __ballot(((m >> lane) & 1) && __popcll(m & below) == slot - before);
-            const int l = __ffsll((long long)at) - 1;
-            const int lo = __builtin_amdgcn_readlane(q.lo[c], l);
-            t = Tile{64 * c + l, lo, __builtin_amdgcn_readlane(q.hi[c], l) - lo};
-        }
-        before += n;
-    }
-    return t;
+    return Tiling(p, 1 << 30, lane).find(p, 1 << 30, slot);
 }
 
 __device__ __forceinline__ int source_row(const Mx4Product &p, int r)
@@ -510,8 +500,8 @@ __global__ __launch_bounds__(256, 2) void product_mx4_kernel(Mx4Product p, int n
 
 // ---------------------------------------------------------------------------------------------
 // Product of bf16 / fp32 rows with MX4 weights: few rows per group, so streaming the weights is what
-// counts.  A wave owns sets of 64 weight rows (with SwiGLU 32 gate rows and their up rows), or with
-// KS > 1 every KS-th step of 128 columns of a set, and streams their codes and scales through a ring
+// counts.  A wave owns a set of 64 weight rows (with SwiGLU 32 gate rows and their up rows), or with
+// KS > 1 every KS-th step of 128 columns of one, and streams their codes and scales through a ring
 // of its own in LDS by direct-to-LDS loads (neighbouring lanes read neighbouring bytes; straight into
 // the matrix cores' lanes every lane would be a cache access of its own).  Only its own loads fill
 // the ring, so it runs without barriers.  The group's rows of x lie in LDS for all sets and waves of
@@ -545,10 +535,10 @@ __device__ __forceinline__ void cut_f32x8(const float *v, bf16x8 (&terms)[3])
     terms[2] = c.v;
 }
 
-constexpr int PW_WAVES = 4, PW_RING = 3;               // waves of a block, stages of a wave's ring
+constexpr int PW_WAVES = 4, PW_RING = 2;               // waves of a block, stages of a wave's ring
 constexpr int PW_STAGE = 64 * 64 + 2 * 64 * 4;         // codes, then scales (two dwords per row) of 128 columns
 constexpr int PW_LOADS = 6;                            // load instructions of a stage
-constexpr int PW_SLAB = 24 * 1024;                     // x
+constexpr int PW_SLAB = 16 * 1024;                     // x
 
 // 2 bytes per lane, each zero-extended into the dword lds + 4 l of lane l.
 __device__ __forceinline__ void lds_dma2(const void *g, uint32_t lds)
@@ -559,7 +549,7 @@ __device__ __forceinline__ void lds_dma2(const void *g, uint32_t lds)
 
 // MT: 16-row fragments of x at a time.
 template <int XK, bool GLU, int MT, int KS>
-__global__ __launch_bounds__(64 * PW_WAVES, 2) void product_wide_kernel(Mx4Product p, int iters)
+__global__ __launch_bounds__(64 * PW_WAVES, MT == 1 ? 3 : 2) void product_wide_kernel(Mx4Product p)
 {
     constexpr int NTERM = XTerms<XK>::N, SETS = PW_WAVES / KS;
     __shared__ __attribute__((aligned(16))) uint8_t s_ring[PW_WAVES * PW_RING * PW_STAGE];
@@ -571,55 +561,41 @@ __global__ __launch_bounds__(64 * PW_WAVES, 2) void product_wide_kernel(Mx4Produ
     constexpr int WO = GLU ? 32 : 64;                      // outputs of a set
     const int F = p.N >> 1, NO = GLU ? F : p.N;
     const int KB = p.K >> 1, KSC = p.K >> 5, steps = (p.K + 127) >> 7;
-    const int ks = wave % KS, set0 = blockIdx.x * iters * SETS + wave / KS;
-    const int nsets = (NO + WO - 1) / WO;
+    const int ks = wave % KS, n0 = (blockIdx.x * SETS + wave / KS) * WO;
+    const bool live = n0 < NO;
     uint8_t *ring = s_ring + wave * PW_RING * PW_STAGE;
     const int drow = lane >> 2, dchunk = 16 * ((lane & 3) ^ ((lane >> 4) & 3));
 
-    // this wave's sets, set0, set0 + SETS, ..: how many of the block's turns it has
-    const int turns = min(iters, max(0, (nsets - set0 + SETS - 1) / SETS));
+    // sources: 4 lanes read a weight row's 64 bytes of a step, lane r row r's scales
+    auto weight_row = [&](int r) {
+        int n = n0 + r;
+        if (GLU) n = min(n0 + (r & 31), F - 1) + ((r & 32) ? F : 0);
+        return (size_t)t.g * p.N + min(n, p.N - 1);
+    };
+    const uint8_t *wsrc[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wsrc[i] = p.w + weight_row(16 * i + drow) * KB;
+    const uint8_t *wsc = p.ws + weight_row(lane) * KSC;
+    // Every call issues PW_LOADS loads, past the end the last step's again, so that the count of
+    // loads in flight holds.
+    auto issue = [&](int s, int buf) {
+        const uint32_t L = lds_addr(ring + buf * PW_STAGE);
+        s = min(s, steps - 1);
+        const int off = s * 64 + dchunk;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            lds_dma16(off < KB ? wsrc[i] + off : reinterpret_cast<const uint8_t *>(&mx4_zeros), L + i * 1024);
+        lds_dma2(wsc + 4 * s, L + 4096);
+        // the last step's missing blocks take the present ones' scales (their codes are zeros)
+        lds_dma2(wsc + (4 * s + 2 < KSC ? 4 * s + 2 : 4 * s), L + 4096 + 256);
+    };
+
     // rows at a time: as many as KS steps of x fit the slab for
     constexpr int RM = PW_SLAB / (2 * NTERM * (KS * 128 + 8)) < 16 * MT ? PW_SLAB / (2 * NTERM * (KS * 128 + 8)) : 16 * MT;
 
     for (int r0 = 0; r0 < t.rows; r0 += RM) {
         const int R = min(RM, t.rows - r0);
-        // ---- the wave's stream of stages: steps ks, ks + KS, .. of set 0, then of set 1, ..
-        int it_p = 0, s_p = ks, buf_p = 0;
-        const uint8_t *wsrc[4], *wsc;
-        auto open_set = [&](int it) {
-            const int n0 = (set0 + it * SETS) * WO;
-            auto weight_row = [&](int r) {
-                int n = n0 + r;
-                if (GLU) n = min(n0 + (r & 31), F - 1) + ((r & 32) ? F : 0);
-                return (size_t)t.g * p.N + min(n, p.N - 1);
-            };
-#pragma unroll
-            for (int i = 0; i < 4; ++i) wsrc[i] = p.w + weight_row(16 * i + drow) * KB;
-            wsc = p.ws + weight_row(lane) * KSC;
-        };
-        // Every call issues PW_LOADS loads, past the stream's end the last step's again, so that the
-        // count of loads in flight holds.
-        auto issue = [&] {
-            const uint32_t L = lds_addr(ring + buf_p * PW_STAGE);
-            const int s = min(s_p, steps - 1), off = s * 64 + dchunk;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                lds_dma16(off < KB ? wsrc[i] + off : reinterpret_cast<const uint8_t *>(&mx4_zeros), L + i * 1024);
-            lds_dma2(wsc + 4 * s, L + 4096);
-            // the last step's missing blocks take the present ones' scales (their codes are zeros)
-            lds_dma2(wsc + (4 * s + 2 < KSC ? 4 * s + 2 : 4 * s), L + 4096 + 256);
-            buf_p = buf_p == PW_RING - 1 ? 0 : buf_p + 1;
-            s_p += KS;
-            if (s_p >= steps && it_p + 1 < turns) {
-                s_p = ks;
-                open_set(++it_p);
-            }
-        };
-        if (turns > 0) {
-            open_set(0);
-#pragma unroll
-            for (int i = 0; i < PW_RING - 1; ++i) issue();
-        }
+        if (live) issue(ks, 0);
 
         // ---- x: [term][row][columns of a slab + 8]; the slab holds all of K where it fits
         if (tid < R) s_src[tid] = source_row(p, t.row0 + r0 + tid);
@@ -655,112 +631,100 @@ __global__ __launch_bounds__(64 * PW_WAVES, 2) void product_wide_kernel(Mx4Produ
         };
 
         int buf = 0;
-        for (int it = 0; it < iters; ++it) {
-            f32x4 acc[4][MT];
+        f32x4 acc[4][MT];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int m = 0; m < MT; ++m) acc[j][m] = zero4();
-            for (int b = 0; b < nslab; ++b) {
-                if (nslab > 1 || it == 0) {
-                    lds_barrier();
-                    load_slab(b);
-                    lds_barrier();
+            for (int m = 0; m < MT; ++m) acc[j][m] = zero4();
+        for (int b = 0; b < nslab; ++b) {
+            lds_barrier();
+            load_slab(b);
+            lds_barrier();
+            const int send = live ? min(steps, (b + 1) * SC) : 0;
+            for (int s = b * SC + ks; s < send; s += KS) {
+                // this stage has landed, and what was read from the next buffer to fill has arrived
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(PW_LOADS * (PW_RING - 2)) : "memory");
+                issue(s + KS, buf ^ 1);
+                const uint8_t *W = ring + buf * PW_STAGE;
+                const uint32_t *S = reinterpret_cast<const uint32_t *>(W + 4096) + (lg >> 1) * 64 + li;
+                buf ^= 1;
+                uint4 w[4];
+                float sc[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    w[j] = *reinterpret_cast<const uint4 *>(W + chunk_at(16 * j + li, lg));
+                    sc[j] = e8m0_f32((S[16 * j] >> (8 * (lg & 1))) & 0xFFu);
                 }
-                const int send = it < turns ? min(steps, (b + 1) * SC) : 0;
-                for (int s = b * SC + ks; s < send; s += KS) {
-                    // this stage has landed, and what was read from the next buffer to fill has arrived
-                    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(PW_LOADS * (PW_RING - 2)) : "memory");
-                    issue();
-                    const uint8_t *W = ring + buf * PW_STAGE;
-                    const uint32_t *S = reinterpret_cast<const uint32_t *>(W + 4096) + (lg >> 1) * 64 + li;
-                    buf = buf == PW_RING - 1 ? 0 : buf + 1;
-                    uint4 w[4];
-                    float sc[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        w[j] = *reinterpret_cast<const uint4 *>(W + chunk_at(16 * j + li, lg));
-                        sc[j] = e8m0_f32((S[16 * j] >> (8 * (lg & 1))) & 0xFFu);
-                    }
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        if (MT > 1 && 16 * m >= R) break;
-                        const uint16_t *X = slab + min(16 * m + li, R - 1) * XS + (s - b * SC) * 128 + 32 * lg;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            bf16x8 xt[NTERM];
-#pragma unroll
-                            for (int k = 0; k < NTERM; ++k) xt[k] = *reinterpret_cast<const bf16x8 *>(X + k * R * XS + 8 * q);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const uint32_t c = q == 0 ? w[j].x : q == 1 ? w[j].y : q == 2 ? w[j].z : w[j].w;
-                                const bf16x8 wb = mx4_bf16x8(c, sc[j]);
-#pragma unroll
-                                for (int k = NTERM - 1; k >= 0; --k) acc[j][m] = mfma16x16x32_bf16(wb, xt[k], acc[j][m]);
-                            }
-                        }
-                    }
-                }
-            }
-            if (it >= turns) continue;
-            // ---- element i of a lane's acc[j][m] is weight row 16 j + 4 lg + i of x row 16 m + li
-            const int n0 = (set0 + it * SETS) * WO;
-            if constexpr (KS > 1) {
-                // the KS waves' sums meet in LDS, in wave order (iters is 1: the rings are idle)
-                float *red = reinterpret_cast<float *>(ring);
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
-                    if (16 * m >= R) break;
-                    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+                    if (MT > 1 && 16 * m >= R) break;
+                    const uint16_t *X = slab + min(16 * m + li, R - 1) * XS + (s - b * SC) * 128 + 32 * lg;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4 *>(red + li * 68 + 16 * j + 4 * lg) = acc[j][m];
-                    lds_barrier();
-                    const int rows = min(16, R - 16 * m);
-                    for (int i = ks * 64 + lane; i < rows * WO; i += KS * 64) {
-                        const int r = i / WO, n = i & (WO - 1);
-                        const float *q = reinterpret_cast<const float *>(s_ring + (wave - ks) * PW_RING * PW_STAGE) + r * 68 + n;
-                        float v = 0.f, u = 0.f;
+                    for (int q = 0; q < 4; ++q) {
+                        bf16x8 xt[NTERM];
 #pragma unroll
-                        for (int k = 0; k < KS; ++k) {
-                            v += q[k * (PW_RING * PW_STAGE / 4)];
-                            if (GLU) u += q[k * (PW_RING * PW_STAGE / 4) + 32];
+                        for (int k = 0; k < NTERM; ++k) xt[k] = *reinterpret_cast<const bf16x8 *>(X + k * R * XS + 8 * q);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t c = q == 0 ? w[j].x : q == 1 ? w[j].y : q == 2 ? w[j].z : w[j].w;
+                            const bf16x8 wb = mx4_bf16x8(c, sc[j]);
+#pragma unroll
+                            for (int k = NTERM - 1; k >= 0; --k) acc[j][m] = mfma16x16x32_bf16(wb, xt[k], acc[j][m]);
                         }
-                        if (n0 + n < NO) {
-                            v = GLU ? silu_fast(v) * u : activate(v, p.act);
-                            const size_t at = (size_t)(t.row0 + r0 + 16 * m + r) * NO + n0 + n;
-                            if (p.otype == X_F32) store1<X_F32>(p, at, v);
-                            else store1<X_BF16>(p, at, v);
-                        }
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    if (16 * m + li >= R) continue;
-                    const size_t row = (size_t)(t.row0 + r0 + 16 * m + li) * NO;
-#pragma unroll
-                    for (int j = 0; j < (GLU ? 2 : 4); ++j) {
-                        const int n = n0 + 16 * j + 4 * lg;
-                        float v[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            v[i] = GLU ? silu_fast(acc[j][m][i]) * acc[(j + 2) & 3][m][i] : activate(acc[j][m][i], p.act);
-                        store4(p, row + n, n, NO, v);
                     }
                 }
             }
         }
         // no load may still be writing LDS
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (!live) continue;
+        // ---- element i of a lane's acc[j][m] is weight row 16 j + 4 lg + i of x row 16 m + li
+        if constexpr (KS > 1) {
+            // the KS waves' sums meet in LDS, in wave order (the rings are idle)
+            float *red = reinterpret_cast<float *>(ring);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                if (16 * m >= R) break;
+                if (m > 0) lds_barrier();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4 *>(red + li * 68 + 16 * j + 4 * lg) = acc[j][m];
+                lds_barrier();
+                const int rows = min(16, R - 16 * m);
+                for (int i = ks * 64 + lane; i < rows * WO; i += KS * 64) {
+                    const int r = i / WO, n = i & (WO - 1);
+                    const float *q = reinterpret_cast<const float *>(s_ring + (wave - ks) * PW_RING * PW_STAGE) + r * 68 + n;
+                    float v = 0.f, u = 0.f;
+#pragma unroll
+                    for (int k = 0; k < KS; ++k) {
+                        v += q[k * (PW_RING * PW_STAGE / 4)];
+                        if (GLU) u += q[k * (PW_RING * PW_STAGE / 4) + 32];
+                    }
+                    if (n0 + n < NO) {
+                        v = GLU ? silu_fast(v) * u : activate(v, p.act);
+                        const size_t at = (size_t)(t.row0 + r0 + 16 * m + r) * NO + n0 + n;
+                        if (p.otype == X_F32) store1<X_F32>(p, at, v);
+                        else store1<X_BF16>(p, at, v);
+                    }
+                }
+            }
+            lds_barrier();                                 // the sums are read before the rings fill again
+        } else {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                if (16 * m + li >= R) continue;
+                const size_t row = (size_t)(t.row0 + r0 + 16 * m + li) * NO;
+#pragma unroll
+                for (int j = 0; j < (GLU ? 2 : 4); ++j) {
+                    const int n = n0 + 16 * j + 4 * lg;
+                    float v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        v[i] = GLU ? silu_fast(acc[j][m][i]) * acc[(j + 2) & 3][m][i] : activate(acc[j][m][i], p.act);
+                    store4(p, row + n, n, NO, v);
+                }
+            }
+        }
     }
-}
-
-template <int XK, bool GLU, int KS>
-hipError_t launch_wide(const Mx4Product &p, int iters, const dim3 &grid, bool many, hipStream_t s)
-{
-    if (many) product_wide_kernel<XK, GLU, XK == X_F32 ? 2 : 4, KS><<<grid, 64 * PW_WAVES, 0, s>>>(p, iters);
-    else product_wide_kernel<XK, GLU, 1, KS><<<grid, 64 * PW_WAVES, 0, s>>>(p, iters);
-    return hipGetLastError();
 }
 
 template <int XK, bool GLU>
@@ -769,15 +733,18 @@ hipError_t launch_wide(const Mx4Product &p, hipStream_t s)
     const int WO = GLU ? 32 : 64, NO = GLU ? p.N / 2 : p.N;
     const int rows = p.Pr + p.S * p.T, G = p.offsets ? p.E + p.S : 1;
     const int slots = rows < G ? rows : G, sets = (NO + WO - 1) / WO;
-    static const int vk = getenv("WK") ? atoi(getenv("WK")) : 0, vi = getenv("WI") ? atoi(getenv("WI")) : 0;
-    int KS = 1, iters = 1;
-    if (vk) KS = vk;
-    if (vi && KS == 1) iters = vi;
-    const int per = PW_WAVES / KS * iters;
-    const dim3 grid((sets + per - 1) / per, slots);
-    // 16 rows at a time where groups hold few, 64 where they hold many
-    const bool many = rows > 16 && rows >= 8 * G;
-    return KS == 1 ? launch_wide<XK, GLU, 1>(p, iters, grid, many, s) : launch_wide<XK, GLU, 4>(p, 1, grid, many, s);
+    const auto grid = [&](int per) { return dim3((sets + per - 1) / per, slots); };
+    // Where groups hold many rows: 64 (fp32: 20, which the slab holds) at a time, not 16.
+    if (rows > 16 && rows >= 8 * G)
+        product_wide_kernel<XK, GLU, XK == X_F32 ? 2 : 4, 1><<<grid(PW_WAVES), 64 * PW_WAVES, 0, s>>>(p);
+    // Four waves share a set's columns while the sets alone leave the GPU short of waves (256 CUs of
+    // 12): one token's 22 sets x 8 experts 9.4 us split and 18.6 whole, 44 x 51 at 8 tokens 25.3 and
+    // 20.6, 42 x 258 at 16 tokens 109 and 91.
+    else if ((long long)sets * slots < 1024)
+        product_wide_kernel<XK, GLU, 1, PW_WAVES><<<grid(1), 64 * PW_WAVES, 0, s>>>(p);
+    else
+        product_wide_kernel<XK, GLU, 1, 1><<<grid(PW_WAVES), 64 * PW_WAVES, 0, s>>>(p);
+    return hipGetLastError();
 }
 
 }  // namespace
