@@ -21,8 +21,9 @@
 namespace moe {
 namespace {
 
-constexpr int BL_THREADS = 256;
-constexpr int BL_BLOCKS = 128;      // partial sums the second kernel adds up
+constexpr int BL_THREADS = 1024;    // of the loss kernels
+constexpr int BG_THREADS = 256;     // of the gradient kernel
+constexpr int BL_BLOCKS = 128;      // most partial sums the second kernel adds up
 constexpr int MAX_EPAD = 512;
 
 template <int LPR>
@@ -82,7 +83,9 @@ __device__ __forceinline__ void load_row(const void *logits, size_t base, int E,
 }
 
 // In place: l becomes p = softmax(l).  Returns lse; `none`: every logit is -inf (p = 0, lse = 0).
-// A NaN or +inf logit makes the row NaN.
+// A NaN or +inf logit makes the row NaN.  The exponent, logarithm and reciprocal instructions are good
+// to 1 ulp; the exponent's rounded argument adds |l - max| roundings of 2^-24 to p, as the fp32 logits
+// themselves carry.
 template <int LPR, int NV>
 __device__ __forceinline__ float softmax_row(float (&l)[NV], int lane, bool &none)
 {
@@ -94,14 +97,14 @@ __device__ __forceinline__ float softmax_row(float (&l)[NV], int lane, bool &non
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        l[i] = none ? 0.f : expf(l[i] - m);
+        l[i] = none ? 0.f : __builtin_amdgcn_exp2f((l[i] - m) * 1.44269504f);
         s += l[i];
     }
     s = group_sum<LPR>(s, lane);
-    const float r = none ? 0.f : 1.f / s;
+    const float r = none ? 0.f : __builtin_amdgcn_rcpf(s);
 #pragma unroll
     for (int i = 0; i < NV; ++i) l[i] *= r;
-    return none ? 0.f : m + logf(s);
+    return none ? 0.f : fmaf(__builtin_amdgcn_logf(s), 0.693147181f, m);
 }
 
 // The block's share of the rows: partial sums of p, of lse^2, and counts.  With one block
@@ -117,15 +120,36 @@ struct BalanceOut {
     int Epad;
 };
 
-// sum over the block of f_e P_e, in thread order within waves and wave order across them
-__device__ __forceinline__ float block_sum(float v, float *s_red, int tid, int nwaves)
+// A row's share of a lane, as it is in memory: loaded a row ahead of its use.  Padding rows are loaded
+// like the others (they lie inside the arrays) and dropped after.
+template <int LT, int LPR, int NJ, int VEC>
+struct Row {
+    float l[NJ * VEC];
+    int id;                 // slot `sub` of the row
+    bool on;
+    __device__ __forceinline__ void load(const void *logits, int t, int T, int E, const int32_t *idx, int k,
+                                         const uint8_t *mask, int sub)
+    {
+        const int r = min(t, T - 1);
+        load_row<LT, LPR, NJ, VEC>(logits, (size_t)r * E, E, sub, l);
+        id = idx[(size_t)r * k + min(sub, k - 1)];
+        on = t < T && (mask == nullptr || mask[r] != 0);
+    }
+    __device__ __forceinline__ void drop_padding()
+    {
+#pragma unroll
+        for (int i = 0; i < NJ * VEC; ++i) l[i] = on ? l[i] : -INFINITY;
+    }
+};
+
+// the block's sum of v: waves by exchange, then in wave order
+__device__ __forceinline__ float block_sum(float v, float *s_red, int tid)
 {
     v = wave_sum(v);
-    __syncthreads();
     if ((tid & 63) == 0) s_red[tid >> 6] = v;
     __syncthreads();
     float t = 0.f;
-    for (int i = 0; i < nwaves; ++i) t += s_red[i];
+    for (int i = 0; i < BL_THREADS / 64; ++i) t += s_red[i];
     return t;
 }
 
@@ -134,68 +158,83 @@ __global__ __launch_bounds__(BL_THREADS) void balance_rows_kernel(const void *__
                                                                   const int32_t *__restrict__ idx, int k,
                                                                   const uint8_t *__restrict__ mask, BalanceOut o)
 {
-    constexpr int NV = NJ * VEC, SUBS = BL_THREADS / LPR;     // rows a block holds at a time
+    constexpr int NV = NJ * VEC, SUBS = BL_THREADS / LPR, NW = BL_THREADS / 64;   // SUBS rows at a time
     __shared__ int s_cnt[MAX_EPAD];
-    __shared__ float s_p[SUBS * LPR * NV];
-    __shared__ float s_z[SUBS];
-    __shared__ int s_n[SUBS];
-    __shared__ float s_red[BL_THREADS / 64];
-    const int tid = threadIdx.x, lane = tid & 63, sub = tid % LPR, row_in = tid / LPR;
+    __shared__ float s_p[NW * LPR * NV];
+    __shared__ float s_z[NW];
+    __shared__ int s_n[NW];
+    __shared__ float s_red[NW];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, sub = tid % LPR, row_in = tid / LPR;
+    const int per = (T + gridDim.x - 1) / gridDim.x;
+    const int t0 = blockIdx.x * per, t1 = min(T, t0 + per);
+    Row<LT, LPR, NJ, VEC> next;
+    next.load(logits, t0 + row_in, T, E, idx, k, mask, sub);
     for (int e = tid; e < E; e += BL_THREADS) s_cnt[e] = 0;
     __syncthreads();
 
     float acc[NV] = {}, z = 0.f;
     int n = 0;
-    const int per = (T + gridDim.x - 1) / gridDim.x;
-    const int t0 = blockIdx.x * per, t1 = min(T, t0 + per);
     for (int tb = t0; tb < t1; tb += SUBS) {
         const int t = tb + row_in;
-        float l[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) l[i] = -INFINITY;
-        const bool on = t < t1 && (mask == nullptr || mask[t] != 0);
-        if (on) load_row<LT, LPR, NJ, VEC>(logits, (size_t)t * E, E, sub, l);
+        Row<LT, LPR, NJ, VEC> r = next;
+        if (tb + SUBS < t1) next.load(logits, t + SUBS, T, E, idx, k, mask, sub);
+        r.on = r.on && t < t1;
+        r.drop_padding();
         bool none;
-        const float lse = softmax_row<LPR, NV>(l, lane, none);
+        const float lse = softmax_row<LPR, NV>(r.l, lane, none);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) acc[i] += l[i];
+        for (int i = 0; i < NV; ++i) acc[i] += r.l[i];
         z += lse * lse;
         if (!none) {
             n += 1;
-            for (int j = sub; j < k; j += LPR) atomicAdd(&s_cnt[clamp_id(idx[(size_t)t * k + j], E)], 1);
+            if (sub < k) atomicAdd(&s_cnt[clamp_id(r.id, E)], 1);
+            for (int j = sub + LPR; j < k; j += LPR) atomicAdd(&s_cnt[clamp_id(idx[(size_t)t * k + j], E)], 1);
         }
     }
+    // the wave's rows, then the waves
 #pragma unroll
-    for (int i = 0; i < NV; ++i) s_p[row_in * LPR * NV + expert_of<LPR, NJ, VEC>(sub, i / VEC, i % VEC)] = acc[i];
-    if (sub == 0) {
-        s_z[row_in] = z;
-        s_n[row_in] = n;
+    for (int s = LPR; s < 64; s <<= 1) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) acc[i] += __uint_as_float(xor_lane_u32(__float_as_uint(acc[i]), s, lane));
+        z += __uint_as_float(xor_lane_u32(__float_as_uint(z), s, lane));
+        n += (int)xor_lane_u32((uint32_t)n, s, lane);
+    }
+    if (lane < LPR) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) s_p[wave * LPR * NV + expert_of<LPR, NJ, VEC>(sub, i / VEC, i % VEC)] = acc[i];
+    }
+    if (lane == 0) {
+        s_z[wave] = z;
+        s_n[wave] = n;
     }
     __syncthreads();
     float zt = 0.f;
     int nt = 0;
-    for (int i = 0; i < SUBS; ++i) {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
         zt += s_z[i];
         nt += s_n[i];
     }
     const bool whole = gridDim.x == 1;
     const float inv = 1.f / (float)max(nt, 1);
     float dot = 0.f;
-    for (int e = tid; e < E; e += BL_THREADS) {
+    if (tid < E) {
         float s = 0.f;
-        for (int i = 0; i < SUBS; ++i) s += s_p[i * LPR * NV + e];
+#pragma unroll
+        for (int i = 0; i < NW; ++i) s += s_p[i * LPR * NV + tid];
+        const int c = s_cnt[tid];
         if (whole) {
             s *= inv;
-            o.counts[e] = s_cnt[e];
-            o.mean_prob[e] = s;
-            dot += (float)s_cnt[e] * (inv / (float)k) * s;
+            o.counts[tid] = c;
+            o.mean_prob[tid] = s;
+            dot = (float)c * (inv / (float)k) * s;
         } else {
-            o.part_p[(size_t)blockIdx.x * o.Epad + e] = s;
-            o.part_c[(size_t)blockIdx.x * o.Epad + e] = s_cnt[e];
+            o.part_p[(size_t)blockIdx.x * o.Epad + tid] = s;
+            o.part_c[(size_t)blockIdx.x * o.Epad + tid] = c;
         }
     }
     if (whole) {
-        dot = block_sum(dot, s_red, tid, BL_THREADS / 64);
+        dot = block_sum(dot, s_red, tid);
         if (tid == 0) {
             o.loss[0] = (float)E * dot;
             o.loss[1] = zt * inv;
@@ -206,22 +245,27 @@ __global__ __launch_bounds__(BL_THREADS) void balance_rows_kernel(const void *__
     }
 }
 
-// Adds the blocks' partial sums in block order within 1024 / Epad strided groups, then the groups.
-__global__ __launch_bounds__(1024) void balance_join_kernel(int blocks, int E, int k, BalanceOut o)
+// Adds the blocks' partial sums: thread groups take every G-th block, four experts a thread, then the
+// groups are added in order.
+__global__ __launch_bounds__(BL_THREADS) void balance_join_kernel(int blocks, int E, int k, BalanceOut o)
 {
-    __shared__ float s_p[1024];
-    __shared__ int s_c[1024];
-    __shared__ float s_red[16];
-    const int tid = threadIdx.x, Ep = o.Epad, G = 1024 / Ep, e = tid % Ep, g = tid / Ep;
-    float s = 0.f;
-    int c = 0;
-    if (e < E && g < G)
+    __shared__ float4 s_p[BL_THREADS];
+    __shared__ int4 s_c[BL_THREADS];
+    __shared__ float s_red[BL_THREADS / 64];
+    const int tid = threadIdx.x, C = o.Epad / 4, G = BL_THREADS / C, c = tid % C, g = tid / C;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    int4 n4 = make_int4(0, 0, 0, 0);
+    if (g < G) {
+#pragma unroll 4
         for (int b = g; b < blocks; b += G) {
-            s += o.part_p[(size_t)b * Ep + e];
-            c += o.part_c[(size_t)b * Ep + e];
+            const float4 u = *reinterpret_cast<const float4 *>(o.part_p + (size_t)b * o.Epad + 4 * c);
+            const int4 v = *reinterpret_cast<const int4 *>(o.part_c + (size_t)b * o.Epad + 4 * c);
+            s.x += u.x; s.y += u.y; s.z += u.z; s.w += u.w;
+            n4.x += v.x; n4.y += v.y; n4.z += v.z; n4.w += v.w;
         }
+    }
     s_p[tid] = s;
-    s_c[tid] = c;
+    s_c[tid] = n4;
     // every wave adds the row counts and the z sums itself
     float zt = 0.f;
     int nt = 0;
@@ -238,15 +282,15 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(int blocks, int E, i
         float P = 0.f;
         int cnt = 0;
         for (int i = 0; i < G; ++i) {
-            P += s_p[i * Ep + tid];
-            cnt += s_c[i * Ep + tid];
+            P += reinterpret_cast<const float *>(s_p + i * C)[tid];
+            cnt += reinterpret_cast<const int *>(s_c + i * C)[tid];
         }
         P *= inv;
         o.counts[tid] = cnt;
         o.mean_prob[tid] = P;
         dot = (float)cnt * (inv / (float)k) * P;
     }
-    dot = block_sum(dot, s_red, tid, 16);
+    dot = block_sum(dot, s_red, tid);
     if (tid == 0) {
         o.loss[0] = (float)E * dot;
         o.loss[1] = zt * inv;
@@ -254,15 +298,27 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(int blocks, int E, i
 }
 
 template <int LT, int LPR, int NJ, int VEC>
-__global__ __launch_bounds__(BL_THREADS) void balance_grad_kernel(
+__global__ __launch_bounds__(BG_THREADS) void balance_grad_kernel(
     const void *__restrict__ logits, int T, int E, const int32_t *__restrict__ idx, int k,
     const uint8_t *__restrict__ mask, const int32_t *__restrict__ counts, const float *__restrict__ d_loss,
     const float *__restrict__ topk_w, const float *__restrict__ d_topk_w, void *__restrict__ d_logits, int gtype)
 {
-    constexpr int NV = NJ * VEC, SUBS = BL_THREADS / LPR;
+    constexpr int NV = NJ * VEC, SUBS = BG_THREADS / LPR;
     __shared__ int s_id[SUBS][MAX_K];
     __shared__ float s_dw[SUBS][MAX_K];
     const int tid = threadIdx.x, lane = tid & 63, sub = tid % LPR, row_in = tid / LPR;
+    const bool wpart = topk_w != nullptr;
+    Row<LT, LPR, NJ, VEC> next;
+    float w_next = 0.f, dw_next = 0.f;
+    auto fetch = [&](int t) {
+        next.load(logits, t, T, E, idx, k, mask, sub);
+        if (wpart) {
+            const size_t at = (size_t)min(t, T - 1) * k + min(sub, k - 1);
+            w_next = topk_w[at];
+            dw_next = d_topk_w[at];
+        }
+    };
+    fetch(blockIdx.x * SUBS + row_in);
     // f of this lane's experts; the counts sum to n k
     float f[NV];
     int c[NV], total = 0;
@@ -278,15 +334,14 @@ __global__ __launch_bounds__(BL_THREADS) void balance_grad_kernel(
 #pragma unroll
     for (int i = 0; i < NV; ++i) f[i] = (float)c[i] * inv_nk;
     const float gb = d_loss[0] * (float)E * inv_n, gz = 2.f * d_loss[1] * inv_n;
-    const bool wpart = topk_w != nullptr;
 
     for (int tb = blockIdx.x * SUBS; tb < T; tb += gridDim.x * SUBS) {
         const int t = tb + row_in;
-        float l[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) l[i] = -INFINITY;
-        const bool on = t < T && (mask == nullptr || mask[t] != 0);
-        if (on) load_row<LT, LPR, NJ, VEC>(logits, (size_t)t * E, E, sub, l);
+        Row<LT, LPR, NJ, VEC> r = next;
+        const float w0 = w_next, dw0 = dw_next;
+        if (tb + (int)gridDim.x * SUBS < T) fetch(t + gridDim.x * SUBS);
+        r.drop_padding();
+        float(&l)[NV] = r.l;
         bool none;
         const float lse = softmax_row<LPR, NV>(l, lane, none);
         float fp = 0.f;
@@ -297,16 +352,17 @@ __global__ __launch_bounds__(BL_THREADS) void balance_grad_kernel(
         for (int i = 0; i < NV; ++i) l[i] = none ? 0.f : l[i] * fmaf(gb, f[i] - fp, gz * lse);
         if (wpart) {
             // the k selected experts' share, added in slot order by the lane that holds the expert
-            float wd = 0.f;
-            for (int j = sub; j < k; j += LPR) {
-                const size_t at = (size_t)min(t, T - 1) * k + j;
-                wd = none ? 0.f : fmaf(topk_w[at], d_topk_w[at], wd);
-            }
+            const size_t base = (size_t)min(t, T - 1) * k;
+            float wd = none || sub >= k ? 0.f : w0 * dw0;
+            for (int j = sub + LPR; j < k; j += LPR) wd = none ? 0.f : fmaf(topk_w[base + j], d_topk_w[base + j], wd);
             wd = group_sum<LPR>(wd, lane);
-            for (int j = sub; j < k; j += LPR) {
-                const size_t at = (size_t)min(t, T - 1) * k + j;
-                s_id[row_in][j] = clamp_id(idx[at], E);
-                s_dw[row_in][j] = none ? 0.f : topk_w[at] * (d_topk_w[at] - wd);
+            if (sub < k) {
+                s_id[row_in][sub] = clamp_id(r.id, E);
+                s_dw[row_in][sub] = none ? 0.f : w0 * (dw0 - wd);
+            }
+            for (int j = sub + LPR; j < k; j += LPR) {
+                s_id[row_in][j] = clamp_id(idx[base + j], E);
+                s_dw[row_in][j] = none ? 0.f : topk_w[base + j] * (d_topk_w[base + j] - wd);
             }
             // a row's lanes sit in one wave, whose LDS accesses stay in order
             __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -378,9 +434,10 @@ int epad(int E) { return (E + 3) / 4 * 4; }
 
 int balance_blocks(int T, int E)
 {
-    // a block takes 16 KB of logits at a time; fewer blocks leave less to add up afterwards
+    // a block holds about 4096 logits at a time; four rounds of them cost less than a second launch,
+    // and fewer blocks leave less to add up
     const long long values = (long long)T * E;
-    const long long b = (values + 4095) / 4096;
+    const long long b = (values + 16383) / 16384;
     return (int)(b < 1 ? 1 : (b > BL_BLOCKS ? BL_BLOCKS : b));
 }
 
@@ -422,10 +479,10 @@ hipError_t launch_balance_grad(const void *logits, int ltype, int T, int E, cons
     ProfScope prof(K_BALANCE, s);
     return by_type(ltype, [&](auto lt) {
         return by_width(E, [&](auto l, auto j, auto v) {
-            constexpr int subs = BL_THREADS / l.value;
+            constexpr int subs = BG_THREADS / l.value;
             const int want = (T + subs - 1) / subs;
-            const int blocks = want < 2048 ? want : 2048;
-            balance_grad_kernel<lt.value, l.value, j.value, v.value><<<blocks, BL_THREADS, 0, s>>>(
+            const int blocks = want < 1024 ? want : 1024;
+            balance_grad_kernel<lt.value, l.value, j.value, v.value><<<blocks, BG_THREADS, 0, s>>>(
                 logits, T, E, idx, k, mask, counts, d_loss, topk_w, d_topk_w, d_logits, gtype);
             return hipGetLastError();
         });
