@@ -267,38 +267,41 @@ _XTYPES = {torch.float32: X_F32, torch.bfloat16: X_BF16, torch.float64: X_F64}
 
 
 def _need(name, t, dtypes, shape, dev):
-    """Raises unless t is a contiguous tensor on GPU `dev` of one of `dtypes` and of `shape` (None: any)."""
+    """Raises unless t is a contiguous tensor on GPU `dev` (an index) of one of `dtypes` and of `shape` (None: any)."""
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and (shape is None or t.shape == shape)
+            and dev >= 0 and t.get_device() == dev and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda or t.device != dev:
-        raise ValueError(f"{name} must be on the GPU the call runs on ({dev}), got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if dev < 0 or t.get_device() != dev:
+        where = f"on GPU {dev}, where the call runs" if dev >= 0 else "on a GPU"
+        raise ValueError(f"{name} must be {where}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _rows_of(name, t, dtypes):
-    """As _need, for the 2-d tensor that decides the call's device."""
+    """As _need, for the 2-d tensor that decides the call's GPU, whose index it returns."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
-    _need(name, t, dtypes, None, t.device)
-    return t.device
+    dev = t.get_device()
+    _need(name, t, dtypes, None, dev)
+    return dev
 
 
 def _run(fn, dev, *args):
-    """Calls the library on `dev`'s current stream, with `dev` the current device."""
+    """Calls the library on GPU `dev`'s current stream, with `dev` the current device."""
     call = getattr(_lib or lib(), fn)
-    index = dev.index
-    if index == torch.cuda.current_device():
-        status = call(*args, torch._C._cuda_getCurrentRawStream(index))
+    if dev == torch.cuda.current_device():
+        status = call(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
-        with torch.cuda.device(index):
-            status = call(*args, torch._C._cuda_getCurrentRawStream(index))
+        with torch.cuda.device(dev):
+            status = call(*args, torch._C._cuda_getCurrentRawStream(dev))
     if status != OK:
         _check(fn, status)
 
@@ -314,8 +317,8 @@ def quantize_rows_mx4(v, want_values: bool = False):
     (float32 or bfloat16); with want_values also the values they stand for, in v's type."""
     dev = _rows_of("v", v, _FLOATS)
     rows, cols = v.shape
-    q = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
-    scale = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
+    q = v.new_empty((rows, cols // 2), dtype=torch.uint8)
+    scale = v.new_empty((rows, cols // 32), dtype=torch.uint8)
     values = torch.empty_like(v) if want_values else None
     _run("moe_quantize_rows_mx4", dev, v.data_ptr(), _XTYPES[v.dtype], rows, cols, q.data_ptr(), scale.data_ptr(),
          values.data_ptr() if want_values else None)
@@ -358,8 +361,7 @@ def matmul_mx4(x, w, w_scales, x_scales=None, offsets=None, perm=None, k: int = 
     scales = None
     if out_dtype == torch.uint8:
         if out is None:
-            out = (torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev),
-                   torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev))
+            out = x.new_empty((rows, cols // 2)), x.new_empty((rows, cols // 32))
         codes, scales = out
         _need("out[0]", codes, _U8, (rows, cols // 2), dev)
         _need("out[1]", scales, _U8, (rows, cols // 32), dev)
@@ -368,7 +370,7 @@ def matmul_mx4(x, w, w_scales, x_scales=None, offsets=None, perm=None, k: int = 
         if out_dtype not in _FLOATS:
             raise TypeError(f"out_dtype must be float32, bfloat16 or uint8, got {out_dtype}")
         if out is None:
-            out = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+            out = x.new_empty((rows, cols), dtype=out_dtype)
         else:
             _need("out", out, (out_dtype,), (rows, cols), dev)
         otype, ptr, sptr = _XTYPES[out_dtype], out.data_ptr(), None
@@ -396,12 +398,12 @@ def balance_loss(logits, topk_idx, mask=None, ws=None):
     dev, T, E, k = _batch(logits, topk_idx, mask)
     L = _lib or lib()
     if ws is None:
-        ws = torch.empty(max(int(L.moe_balance_workspace_bytes(T, E)), 256), dtype=torch.uint8, device=dev)
+        ws = topk_idx.new_empty(max(L.moe_balance_workspace_bytes(T, E), 256), dtype=torch.uint8)
     else:
         _need("ws", ws, _U8, None, dev)
-    loss = torch.empty(2, dtype=torch.float32, device=dev)
-    counts = torch.empty(E, dtype=torch.int32, device=dev)
-    mean_prob = torch.empty(E, dtype=torch.float32, device=dev)
+    loss = topk_idx.new_empty(2, dtype=torch.float32)
+    counts = topk_idx.new_empty(E)
+    mean_prob = topk_idx.new_empty(E, dtype=torch.float32)
     _run("moe_balance_loss", dev, logits.data_ptr(), _XTYPES[logits.dtype], T, E, topk_idx.data_ptr(), k,
          None if mask is None else mask.data_ptr(), loss.data_ptr(), counts.data_ptr(), mean_prob.data_ptr(),
          ws.data_ptr(), ws.numel())
@@ -424,7 +426,7 @@ def balance_loss_backward(logits, topk_idx, counts, d_loss, topk_w=None, d_topk_
         grad_dtype = torch.float32 if logits.dtype == torch.float64 else logits.dtype
     if grad_dtype not in _FLOATS:
         raise TypeError(f"grad_dtype must be float32 or bfloat16, got {grad_dtype}")
-    d_logits = torch.empty((T, E), dtype=grad_dtype, device=dev)
+    d_logits = torch.empty_like(logits, dtype=grad_dtype)
     _run("moe_balance_loss_backward", dev, logits.data_ptr(), _XTYPES[logits.dtype], T, E, topk_idx.data_ptr(), k,
          None if mask is None else mask.data_ptr(), counts.data_ptr(), d_loss.data_ptr(),
          None if topk_w is None else topk_w.data_ptr(), None if topk_w is None else d_topk_w.data_ptr(),
