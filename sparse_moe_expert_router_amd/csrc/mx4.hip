@@ -282,7 +282,7 @@ __device__ __forceinline__ i32x8v code_reg(const uint4 &v)
 
 // Where a stage keeps 16-byte chunk c of row r (64-byte rows): the 16 rows that the 16 lanes of a
 // fragment read at once fall on different banks.
-__device__ __forceinline__ int chunk_at(int r, int c) { return r * 64 + 16 * (c ^ ((r >> 2) & 3)); }
+__device__ __forceinline__ int chunk64_at(int r, int c) { return r * 64 + 16 * (c ^ ((r >> 2) & 3)); }
 
 // Scales 16 q .. 16 q + 15 of a row (`row`: its scales, n in all), 1 for those past the end.  Rows of
 // scales start at even addresses only.
@@ -374,12 +374,12 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
         int sa[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            a[j] = code_reg(*reinterpret_cast<const uint4 *>(W + wave * 4096 + chunk_at(16 * j + li, lg)));
+            a[j] = code_reg(*reinterpret_cast<const uint4 *>(W + wave * 4096 + chunk64_at(16 * j + li, lg)));
             sa[j] = (int)(WS[64 * j] >> sh);
         }
 #pragma unroll
         for (int f = 0; f < MF; ++f) {
-            const i32x8v b = code_reg(*reinterpret_cast<const uint4 *>(X + chunk_at(16 * f + li, lg)));
+            const i32x8v b = code_reg(*reinterpret_cast<const uint4 *>(X + chunk64_at(16 * f + li, lg)));
             const int sb = (int)(XS[64 * f] >> sh);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -500,8 +500,8 @@ __global__ __launch_bounds__(256, 2) void product_mx4_kernel(Mx4Product p, int n
 
 // ---------------------------------------------------------------------------------------------
 // Product of bf16 / fp32 rows with MX4 weights: few rows per group, so streaming the weights is what
-// counts.  A wave owns a set of 64 weight rows (with SwiGLU 32 gate rows and their up rows), or with
-// KS > 1 every KS-th step of 128 columns of one, and streams their codes and scales through a ring
+// counts.  A wave owns a set of 32 weight rows (with SwiGLU 16 gate rows and their up rows), or with
+// KS > 1 every KS-th stage of 256 columns of one, and streams their codes and scales through a ring
 // of its own in LDS by direct-to-LDS loads (neighbouring lanes read neighbouring bytes; straight into
 // the matrix cores' lanes every lane would be a cache access of its own).  Only its own loads fill
 // the ring, so it runs without barriers.  The group's rows of x lie in LDS for all sets and waves of
@@ -535,10 +535,11 @@ __device__ __forceinline__ void cut_f32x8(const float *v, bf16x8 (&terms)[3])
     terms[2] = c.v;
 }
 
+// The same with 128-byte rows.
+__device__ __forceinline__ int chunk_at(int r, int c) { return r * 128 + 16 * (c ^ ((r >> 1) & 7)); }
+
 constexpr int PW_WAVES = 4, PW_RING = 2;               // waves of a block, stages of a wave's ring
-constexpr int PW_STAGE = 64 * 64 + 2 * 64 * 4;         // codes, then scales (two dwords per row) of 128 columns
-constexpr int PW_LOADS = 6;                            // load instructions of a stage
-constexpr int PW_SLAB = 16 * 1024;                     // x
+constexpr int PW_STAGE = 32 * 128 + 4 * 32 * 4;        // codes, then scales (four dwords per row) of 256 columns
 
 // 2 bytes per lane, each zero-extended into the dword lds + 4 l of lane l.
 __device__ __forceinline__ void lds_dma2(const void *g, uint32_t lds)
@@ -549,49 +550,51 @@ __device__ __forceinline__ void lds_dma2(const void *g, uint32_t lds)
 
 // MT: 16-row fragments of x at a time.
 template <int XK, bool GLU, int MT, int KS>
-__global__ __launch_bounds__(64 * PW_WAVES, MT == 1 ? 3 : 2) void product_wide_kernel(Mx4Product p)
+__global__ __launch_bounds__(64 * PW_WAVES, KS == 1 && MT == 1 ? 3 : 2) void product_wide_kernel(Mx4Product p)
 {
     constexpr int NTERM = XTerms<XK>::N, SETS = PW_WAVES / KS;
     __shared__ __attribute__((aligned(16))) uint8_t s_ring[PW_WAVES * PW_RING * PW_STAGE];
+    // x: three blocks to a CU where they are many and their groups small, else two
+    constexpr int PW_SLAB = (KS == 1 && MT == 1 ? 16 : 40) * 1024;
     __shared__ __attribute__((aligned(16))) uint8_t s_slab[PW_SLAB];
     __shared__ int s_src[16 * MT];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, li = lane & 15, lg = lane >> 4;
     const Tile t = find_slot(p, blockIdx.y, lane);
     if (t.rows < 1) return;
-    constexpr int WO = GLU ? 32 : 64;                      // outputs of a set
+    constexpr int WO = GLU ? 16 : 32, TN = 2;              // outputs of a set, 16-row weight tiles
     const int F = p.N >> 1, NO = GLU ? F : p.N;
-    const int KB = p.K >> 1, KSC = p.K >> 5, steps = (p.K + 127) >> 7;
+    const int KB = p.K >> 1, KSC = p.K >> 5, steps = (p.K + 255) >> 8;   // stages of 256 columns
     const int ks = wave % KS, n0 = (blockIdx.x * SETS + wave / KS) * WO;
     const bool live = n0 < NO;
     uint8_t *ring = s_ring + wave * PW_RING * PW_STAGE;
-    const int drow = lane >> 2, dchunk = 16 * ((lane & 3) ^ ((lane >> 4) & 3));
-
-    // sources: 4 lanes read a weight row's 64 bytes of a step, lane r row r's scales
+    // sources: 8 lanes read a weight row's 128 bytes of a stage; lanes r and r + 32 the scales of row r
     auto weight_row = [&](int r) {
         int n = n0 + r;
-        if (GLU) n = min(n0 + (r & 31), F - 1) + ((r & 32) ? F : 0);
+        if (GLU) n = min(n0 + (r & 15), F - 1) + ((r & 16) ? F : 0);
         return (size_t)t.g * p.N + min(n, p.N - 1);
     };
     const uint8_t *wsrc[4];
+    int dchunk[2];                                         // of even and odd instructions (8 rows each)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wsrc[i] = p.w + weight_row(16 * i + drow) * KB;
-    const uint8_t *wsc = p.ws + weight_row(lane) * KSC;
-    // Every call issues PW_LOADS loads, past the end the last step's again, so that the count of
-    // loads in flight holds.
+    for (int i = 0; i < 4; ++i) wsrc[i] = p.w + weight_row(8 * i + (lane >> 3)) * KB;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) dchunk[i] = 16 * ((lane & 7) ^ (((8 * i + (lane >> 3)) >> 1) & 7));
+    const uint8_t *wsc = p.ws + weight_row(lane & 31) * KSC;
     auto issue = [&](int s, int buf) {
+        if (s >= steps) return;
         const uint32_t L = lds_addr(ring + buf * PW_STAGE);
-        s = min(s, steps - 1);
-        const int off = s * 64 + dchunk;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+            const int off = s * 128 + dchunk[i & 1];
             lds_dma16(off < KB ? wsrc[i] + off : reinterpret_cast<const uint8_t *>(&mx4_zeros), L + i * 1024);
-        lds_dma2(wsc + 4 * s, L + 4096);
-        // the last step's missing blocks take the present ones' scales (their codes are zeros)
-        lds_dma2(wsc + (4 * s + 2 < KSC ? 4 * s + 2 : 4 * s), L + 4096 + 256);
+        }
+        // blocks past the end take the row's last scales (their codes are zeros)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) lds_dma2(wsc + min(8 * s + 4 * h + ((lane >> 4) & 2), KSC - 2), L + 4096 + 256 * h);
     };
 
     // rows at a time: as many as KS steps of x fit the slab for
-    constexpr int RM = PW_SLAB / (2 * NTERM * (KS * 128 + 8)) < 16 * MT ? PW_SLAB / (2 * NTERM * (KS * 128 + 8)) : 16 * MT;
+    constexpr int RM = PW_SLAB / (2 * NTERM * (KS * 256 + 8)) < 16 * MT ? PW_SLAB / (2 * NTERM * (KS * 256 + 8)) : 16 * MT;
 
     for (int r0 = 0; r0 < t.rows; r0 += RM) {
         const int R = min(RM, t.rows - r0);
@@ -599,12 +602,12 @@ __global__ __launch_bounds__(64 * PW_WAVES, MT == 1 ? 3 : 2) void product_wide_k
 
         // ---- x: [term][row][columns of a slab + 8]; the slab holds all of K where it fits
         if (tid < R) s_src[tid] = source_row(p, t.row0 + r0 + tid);
-        const int SC = (PW_SLAB / (2 * NTERM * R) - 8) / 128 / KS * KS;   // steps of a slab, at least KS
-        const int XS = min(SC, steps) * 128 + 8;                   // bf16 values of a slab row
+        const int SC = (PW_SLAB / (2 * NTERM * R) - 8) / 256 / KS * KS;   // stages of a slab, at least KS
+        const int XS = min(SC, steps) * 256 + 8;                   // bf16 values of a slab row
         const int nslab = (steps + SC - 1) / SC;
         uint16_t *slab = reinterpret_cast<uint16_t *>(s_slab);
         auto load_slab = [&](int b) {
-            const int c0 = b * SC * 128, pieces = (min(steps, (b + 1) * SC) * 128 - c0) / 8;
+            const int c0 = b * SC * 256, pieces = (min(steps, (b + 1) * SC) * 256 - c0) / 8;
             for (int i = tid; i < R * pieces; i += 64 * PW_WAVES) {
                 const int r = i / pieces, c = 8 * (i - r * pieces);
                 const size_t at = (size_t)s_src[r] * p.K + c0 + c;
@@ -631,9 +634,9 @@ __global__ __launch_bounds__(64 * PW_WAVES, MT == 1 ? 3 : 2) void product_wide_k
         };
 
         int buf = 0;
-        f32x4 acc[4][MT];
+        f32x4 acc[TN][MT];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < TN; ++j)
 #pragma unroll
             for (int m = 0; m < MT; ++m) acc[j][m] = zero4();
         for (int b = 0; b < nslab; ++b) {
@@ -642,34 +645,37 @@ __global__ __launch_bounds__(64 * PW_WAVES, MT == 1 ? 3 : 2) void product_wide_k
             lds_barrier();
             const int send = live ? min(steps, (b + 1) * SC) : 0;
             for (int s = b * SC + ks; s < send; s += KS) {
-                // this stage has landed, and what was read from the next buffer to fill has arrived
-                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(PW_LOADS * (PW_RING - 2)) : "memory");
+                // this stage has landed, and what was read from the buffer to fill next has arrived
+                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
                 issue(s + KS, buf ^ 1);
                 const uint8_t *W = ring + buf * PW_STAGE;
-                const uint32_t *S = reinterpret_cast<const uint32_t *>(W + 4096) + (lg >> 1) * 64 + li;
                 buf ^= 1;
-                uint4 w[4];
-                float sc[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    w[j] = *reinterpret_cast<const uint4 *>(W + chunk_at(16 * j + li, lg));
-                    sc[j] = e8m0_f32((S[16 * j] >> (8 * (lg & 1))) & 0xFFu);
-                }
+                for (int u = 0; u < 2; ++u) {              // 128 columns
+                    const uint32_t *S = reinterpret_cast<const uint32_t *>(W + 4096) + 64 * u + (lg >> 1) * 32 + li;
+                    uint4 w[TN];
+                    float sc[TN];
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    if (MT > 1 && 16 * m >= R) break;
-                    const uint16_t *X = slab + min(16 * m + li, R - 1) * XS + (s - b * SC) * 128 + 32 * lg;
+                    for (int j = 0; j < TN; ++j) {
+                        w[j] = *reinterpret_cast<const uint4 *>(W + chunk_at(16 * j + li, 4 * u + lg));
+                        sc[j] = e8m0_f32((S[16 * j] >> (8 * (lg & 1))) & 0xFFu);
+                    }
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        bf16x8 xt[NTERM];
+                    for (int m = 0; m < MT; ++m) {
+                        if (MT > 1 && 16 * m >= R) break;
+                        const uint16_t *X = slab + min(16 * m + li, R - 1) * XS + (s - b * SC) * 256 + 128 * u + 32 * lg;
 #pragma unroll
-                        for (int k = 0; k < NTERM; ++k) xt[k] = *reinterpret_cast<const bf16x8 *>(X + k * R * XS + 8 * q);
+                        for (int q = 0; q < 4; ++q) {
+                            bf16x8 xt[NTERM];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint32_t c = q == 0 ? w[j].x : q == 1 ? w[j].y : q == 2 ? w[j].z : w[j].w;
-                            const bf16x8 wb = mx4_bf16x8(c, sc[j]);
+                            for (int k = 0; k < NTERM; ++k) xt[k] = *reinterpret_cast<const bf16x8 *>(X + k * R * XS + 8 * q);
 #pragma unroll
-                            for (int k = NTERM - 1; k >= 0; --k) acc[j][m] = mfma16x16x32_bf16(wb, xt[k], acc[j][m]);
+                            for (int j = 0; j < TN; ++j) {
+                                const uint32_t c = q == 0 ? w[j].x : q == 1 ? w[j].y : q == 2 ? w[j].z : w[j].w;
+                                const bf16x8 wb = mx4_bf16x8(c, sc[j]);
+#pragma unroll
+                                for (int k = NTERM - 1; k >= 0; --k) acc[j][m] = mfma16x16x32_bf16(wb, xt[k], acc[j][m]);
+                            }
                         }
                     }
                 }
@@ -687,17 +693,17 @@ __global__ __launch_bounds__(64 * PW_WAVES, MT == 1 ? 3 : 2) void product_wide_k
                 if (16 * m >= R) break;
                 if (m > 0) lds_barrier();
 #pragma unroll
-                for (int j = 0; j < 4; ++j) *reinterpret_cast<f32x4 *>(red + li * 68 + 16 * j + 4 * lg) = acc[j][m];
+                for (int j = 0; j < TN; ++j) *reinterpret_cast<f32x4 *>(red + li * 36 + 16 * j + 4 * lg) = acc[j][m];
                 lds_barrier();
                 const int rows = min(16, R - 16 * m);
                 for (int i = ks * 64 + lane; i < rows * WO; i += KS * 64) {
                     const int r = i / WO, n = i & (WO - 1);
-                    const float *q = reinterpret_cast<const float *>(s_ring + (wave - ks) * PW_RING * PW_STAGE) + r * 68 + n;
+                    const float *q = reinterpret_cast<const float *>(s_ring + (wave - ks) * PW_RING * PW_STAGE) + r * 36 + n;
                     float v = 0.f, u = 0.f;
 #pragma unroll
                     for (int k = 0; k < KS; ++k) {
                         v += q[k * (PW_RING * PW_STAGE / 4)];
-                        if (GLU) u += q[k * (PW_RING * PW_STAGE / 4) + 32];
+                        if (GLU) u += q[k * (PW_RING * PW_STAGE / 4) + 16];
                     }
                     if (n0 + n < NO) {
                         v = GLU ? silu_fast(v) * u : activate(v, p.act);
@@ -714,12 +720,12 @@ __global__ __launch_bounds__(64 * PW_WAVES, MT == 1 ? 3 : 2) void product_wide_k
                 if (16 * m + li >= R) continue;
                 const size_t row = (size_t)(t.row0 + r0 + 16 * m + li) * NO;
 #pragma unroll
-                for (int j = 0; j < (GLU ? 2 : 4); ++j) {
+                for (int j = 0; j < (GLU ? 1 : 2); ++j) {
                     const int n = n0 + 16 * j + 4 * lg;
                     float v[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        v[i] = GLU ? silu_fast(acc[j][m][i]) * acc[(j + 2) & 3][m][i] : activate(acc[j][m][i], p.act);
+                        v[i] = GLU ? silu_fast(acc[j][m][i]) * acc[1][m][i] : activate(acc[j][m][i], p.act);
                     store4(p, row + n, n, NO, v);
                 }
             }
@@ -730,7 +736,7 @@ __global__ __launch_bounds__(64 * PW_WAVES, MT == 1 ? 3 : 2) void product_wide_k
 template <int XK, bool GLU>
 hipError_t launch_wide(const Mx4Product &p, hipStream_t s)
 {
-    const int WO = GLU ? 32 : 64, NO = GLU ? p.N / 2 : p.N;
+    const int WO = GLU ? 16 : 32, NO = GLU ? p.N / 2 : p.N;
     const int rows = p.Pr + p.S * p.T, G = p.offsets ? p.E + p.S : 1;
     const int slots = rows < G ? rows : G, sets = (NO + WO - 1) / WO;
     const auto grid = [&](int per) { return dim3((sets + per - 1) / per, slots); };
@@ -738,9 +744,8 @@ hipError_t launch_wide(const Mx4Product &p, hipStream_t s)
     if (rows > 16 && rows >= 8 * G)
         product_wide_kernel<XK, GLU, XK == X_F32 ? 2 : 4, 1><<<grid(PW_WAVES), 64 * PW_WAVES, 0, s>>>(p);
     // Four waves share a set's columns while the sets alone leave the GPU short of waves (256 CUs of
-    // 12): one token's 22 sets x 8 experts 9.4 us split and 18.6 whole, 44 x 51 at 8 tokens 25.3 and
-    // 20.6, 42 x 258 at 16 tokens 109 and 91.
-    else if ((long long)sets * slots < 1024)
+    // 12): one token's 44 sets x 8 experts 9.0 us split and 18 whole, 88 x 51 at 8 tokens 37 and 19.
+    else if ((long long)sets * slots < 2048)
         product_wide_kernel<XK, GLU, 1, PW_WAVES><<<grid(1), 64 * PW_WAVES, 0, s>>>(p);
     else
         product_wide_kernel<XK, GLU, 1, 1><<<grid(PW_WAVES), 64 * PW_WAVES, 0, s>>>(p);
