@@ -4,7 +4,7 @@
 //     out[r] = act(W[g] x[src(r)]),   src(r) = perm[r] / k,   or r without a permutation,
 // with W[g] of N rows by K columns.  Two kernels:
 //  - product_mx4_kernel: x in MX4 too.  E2M1 x E2M1 with both block scales applied inside
-//    v_mfma_scale_f32_16x16x128_f8f6f4; for batches of rows.
+//    v_mfma_scale_f32_32x32x64_f8f6f4; for batches of rows.
 //  - product_wide_kernel: x in bf16 or fp32, entering exactly; weights widened to bf16; for few
 //    rows per group, where streaming the weights is all that counts.
 #include <hip/hip_runtime.h>
@@ -308,8 +308,7 @@ __device__ const uint4 mx4_zeros = {0, 0, 0, 0};
 template <bool GLU, int OT, int MG>
 __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t, int nt, uint8_t *lds)
 {
-    constexpr int MF = 2 * MG;           // 16-row fragments
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, li = lane & 15, lg = lane >> 4;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, li = lane & 31, lh = lane >> 5;
     const int F = p.N >> 1, NO = GLU ? F : p.N;
     const int KB = p.K >> 1, KSC = p.K >> 5;              // bytes of codes, of scales per row
     const int steps = (p.K + 127) >> 7;                   // the last one may hold 64 columns
@@ -327,18 +326,12 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
 
     // ---- sources: 4 lanes read a row's 64 bytes; instruction i of a wave fills 16 rows.  Rows past the
     // tile's or the matrix's end read the last one, so that every wave issues the same loads.
-    constexpr int XI = (MF + 3) / 4;                      // x code instructions of a wave
+    constexpr int XI = (MG + 1) / 2;                      // x code instructions of a wave
     const uint8_t *wsrc[4], *xsrc[XI];
     const int drow = lane >> 2, dchunk = 16 * ((lane & 3) ^ ((lane >> 4) & 3));   // (row >> 2) & 3 of row = lane / 4
     auto x_row = [&](int r) { return (size_t)source_row(p, t.row0 + min(r, t.rows - 1)); };
 #pragma unroll
     for (int i = 0; i < 4; ++i) wsrc[i] = p.w + weight_row(64 * wave + 16 * i + drow) * KB;
-#pragma unroll
-    for (int i = 0; i < XI; ++i) xsrc[i] = static_cast<const uint8_t *>(p.x) + x_row(16 * (wave + 4 * i) + drow) * KB;
-    // thread r: the scales of weight row r and (the first 128) of row r
-    const uint8_t *wsc = p.ws + weight_row(tid) * KSC;
-    const uint8_t *xsc = p.xs + x_row(tid & (PB_M - 1)) * KSC;
-
     uint8_t *xlds = lds + PB_WBUF * PB_WST, *slds = xlds + PB_XBUF * PB_XST;
     auto issue_w = [&](int s, int buf) {
         const uint32_t L = lds_addr(lds + buf * PB_WST);
@@ -353,38 +346,60 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
 #pragma unroll
         for (int i = 0; i < XI; ++i) lds_dma16(xsrc[i] + off, L + (wave + 4 * i) * 1024);
     };
+    // the weights need only the group: they are on their way while the rows' places are looked up
+    issue_w(0, 0);
+    issue_w(1, 1);
+    // thread r: the scales of weight row r and (the first 128) of row r
+    const uint8_t *wsc = p.ws + weight_row(tid) * KSC;
+    uint4 sw = scales16(wsc, 0, KSC);
+#pragma unroll
+    for (int i = 0; i < XI; ++i) xsrc[i] = static_cast<const uint8_t *>(p.x) + x_row(16 * (wave + 4 * i) + drow) * KB;
+    issue_x(0);
+    const uint8_t *xsc = p.xs + x_row(tid & (PB_M - 1)) * KSC;
+    uint4 sx = scales16(xsc, 0, KSC);
     auto put_scales = [&](int q, const uint4 &w, const uint4 &x) {
         uint4 *S = reinterpret_cast<uint4 *>(slds + (q & 1) * PB_SST);
         S[tid] = w;
         if (tid < PB_M) S[PB_N + tid] = x;
     };
 
-    f32x4 acc[4][MF];
+    f32x16v acc[2][MG];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int f = 0; f < MF; ++f) acc[j][f] = zero4();
+        for (int f = 0; f < MG; ++f)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[j][f][i] = 0.f;
 
+    // A lane holds half a row's 64 columns, blocks 2 u + lh of the step: with the row's scales shifted by
+    // its half, byte 2 u is the one.
     auto step = [&](int s, int buf) {
-        const uint8_t *X = xlds + (s & 1) * PB_XST, *W = lds + buf * PB_WST;
-        const uint32_t *S = reinterpret_cast<const uint32_t *>(slds + ((s >> 2) & 1) * PB_SST) + (s & 3);
-        const uint32_t *WS = S + 4 * (64 * wave + li), *XS = S + 4 * (PB_N + li);
-        const int sh = 8 * lg;
-        i32x8v a[4];
-        int sa[4];
+        const uint8_t *X = xlds + (s & 1) * PB_XST, *W = lds + buf * PB_WST + wave * 4096;
+        const uint32_t *S = reinterpret_cast<const uint32_t *>(slds + ((s >> 2) & 1) * PB_SST) + (s & 3) + 4 * li;
+        const uint32_t *WS = S + 256 * wave, *XS = S + 4 * PB_N;
+        int sa[2], sb[MG];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            a[j] = code_reg(*reinterpret_cast<const uint4 *>(W + wave * 4096 + chunk64_at(16 * j + li, lg)));
-            sa[j] = (int)(WS[64 * j] >> sh);
+        for (int j = 0; j < 2; ++j) sa[j] = (int)(WS[128 * j] >> (8 * lh));
+#pragma unroll
+        for (int f = 0; f < MG; ++f) sb[f] = (int)(XS[128 * f] >> (8 * lh));
+        i32x8v a[2][2], b[2][MG];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) a[u][j] = code_reg(*reinterpret_cast<const uint4 *>(W + chunk64_at(32 * j + li, 2 * u + lh)));
+#pragma unroll
+            for (int f = 0; f < MG; ++f) b[u][f] = code_reg(*reinterpret_cast<const uint4 *>(X + chunk64_at(32 * f + li, 2 * u + lh)));
         }
 #pragma unroll
-        for (int f = 0; f < MF; ++f) {
-            const i32x8v b = code_reg(*reinterpret_cast<const uint4 *>(X + chunk64_at(16 * f + li, lg)));
-            const int sb = (int)(XS[64 * f] >> sh);
+        for (int f = 0; f < MG; ++f)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                acc[j][f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a[j], b, acc[j][f], 4, 4, 0, sa[j], 0, sb);
-        }
+            for (int j = 0; j < 2; ++j)
+                acc[j][f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[0][j], b[0][f], acc[j][f], 4, 4, 0, sa[j], 0, sb[f]);
+#pragma unroll
+        for (int f = 0; f < MG; ++f)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                acc[j][f] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[1][j], b[1][f], acc[j][f], 4, 4, 2, sa[j], 2, sb[f]);
     };
 
     // Weights are asked for two steps ahead, x one step ahead.  At the top of step s the newest
@@ -392,11 +407,8 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
     // issues the same number of loads (past the end the last step's again), so the count holds.
     // Scales go through registers, 16 of a row at a time: asked for at the first of four steps, put
     // into the other LDS buffer at the last.
-    uint4 sw = scales16(wsc, 0, KSC), sx = scales16(xsc, 0, KSC);
-    issue_x(0);
-    issue_w(0, 0);
-    issue_w(1, 1);
     put_scales(0, sw, sx);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     int buf = 0;
     for (int s = 0; s < steps; ++s) {
         // stage s has landed in every wave, and every wave has left the buffers filled next
@@ -417,40 +429,42 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     if (!live) return;
 
-    // ---- epilogue: lane l, element i of acc[j][f] is output 16 j + 4 (l / 16) + i of row 16 f + l % 16.
-    // Each fragment's 16 rows turn round in the wave's own part of LDS, so that neighbouring lanes
-    // store neighbouring outputs of a row.
-    constexpr int RS = WO + 4, JN = GLU ? 2 : 4;
-    float *T = reinterpret_cast<float *>(lds) + wave * 16 * (64 + 4);
+    // ---- epilogue: lane l, element i of acc[j][f] is output 32 j + 8 (i / 4) + 4 (l / 32) + i % 4 of row
+    // 32 f + l % 32.  Each fragment's 32 rows turn round in the wave's own part of LDS, so that
+    // neighbouring lanes store neighbouring outputs of a row.
+    constexpr int RS = WO + 4;
+    float *T = reinterpret_cast<float *>(lds) + wave * 32 * (64 + 4);
     const bool whole = NO % (OT == X_F32 ? 4 : 8) == 0;
 #pragma unroll
-    for (int f = 0; f < MF; ++f) {
-        if (16 * f >= t.rows) break;
+    for (int f = 0; f < MG; ++f) {
 #pragma unroll
-        for (int j = 0; j < JN; ++j) {
-            f32x4 v;
+        for (int j = 0; j < (GLU ? 1 : 2); ++j)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = GLU ? silu_fast(acc[j][f][i]) * acc[(j + 2) & 3][f][i] : activate(acc[j][f][i], p.act);
-            *reinterpret_cast<f32x4 *>(T + li * RS + 16 * j + 4 * lg) = v;
-        }
+            for (int i = 0; i < 16; i += 4) {
+                f32x4 v;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v[k] = GLU ? silu_fast(acc[0][f][i + k]) * acc[1][f][i + k] : activate(acc[j][f][i + k], p.act);
+                *reinterpret_cast<f32x4 *>(T + li * RS + 32 * j + 2 * i + 4 * lh) = v;
+            }
         __builtin_amdgcn_wave_barrier();
-        const int r0 = t.row0 + 16 * f, rn = t.rows - 16 * f;
+        const int r0 = t.row0 + 32 * f, rn = t.rows - 32 * f;
         if (OT != X_MX4 && !whole) {
 #pragma unroll 1
-            for (int i = lane; i < 16 * WO; i += 64) {
+            for (int i = lane; i < 32 * WO; i += 64) {
                 const int r = i / WO, n = i & (WO - 1);
                 if (r < rn && n0 + n < NO) store1<OT>(p, (size_t)(r0 + r) * NO + n0 + n, T[r * RS + n]);
             }
         } else if (OT == X_F32) {
 #pragma unroll
-            for (int i = 0; i < 16 * WO / 4; i += 64) {
+            for (int i = 0; i < 32 * WO / 4; i += 64) {
                 const int r = (i + lane) / (WO / 4), n = 4 * ((i + lane) & (WO / 4 - 1));
                 const f32x4 v = *reinterpret_cast<const f32x4 *>(T + r * RS + n);
                 if (r < rn && n0 + n < NO) *reinterpret_cast<f32x4 *>(static_cast<float *>(p.out) + (size_t)(r0 + r) * NO + n0 + n) = v;
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 16 * WO / 8; i += 64) {
+            for (int i = 0; i < 32 * WO / 8; i += 64) {
                 const int r = (i + lane) / (WO / 8), n = 8 * ((i + lane) & (WO / 8 - 1));
                 float u[8];
                 *reinterpret_cast<f32x4 *>(u) = *reinterpret_cast<const f32x4 *>(T + r * RS + n);

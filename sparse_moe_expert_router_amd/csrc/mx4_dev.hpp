@@ -8,6 +8,7 @@ namespace moe {
 
 typedef int i32x8v __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
+typedef float f32x16v __attribute__((ext_vector_type(16)));
 typedef float f32x2v __attribute__((ext_vector_type(2)));
 
 constexpr int MX_BLOCK = 32;
