@@ -344,10 +344,14 @@ def matmul_mx4(x, w, w_scales, x_scales=None, offsets=None, perm=None, k: int = 
         raise ValueError("x_scales goes with x as MX4 codes only")
     if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
         raise ValueError("w must be [E, N, K/2] or [N, K/2]")
-    lead = w.shape[:-1]
-    _need("w", w, _U8, (*lead, K // 2), dev)
-    _need("w_scales", w_scales, _U8, (*lead, K // 32), dev)
-    E, N = (lead[0], lead[1]) if len(lead) == 2 else (1, lead[0])
+    if w.dim() == 3:
+        E, N, _ = w.shape
+        _need("w", w, _U8, (E, N, K // 2), dev)
+        _need("w_scales", w_scales, _U8, (E, N, K // 32), dev)
+    else:
+        E, N = 1, w.shape[0]
+        _need("w", w, _U8, (N, K // 2), dev)
+        _need("w_scales", w_scales, _U8, (N, K // 32), dev)
     if offsets is not None:
         _need("offsets", offsets, _I32, (E + 1,), dev)
     elif E != 1:
@@ -396,17 +400,25 @@ def balance_loss(logits, topk_idx, mask=None, ws=None):
     [E]) of router logits [T, E] (float32, bfloat16 or float64) and the selected ids [T, k]; mask
     [T] (bool or uint8): False for padding."""
     dev, T, E, k = _batch(logits, topk_idx, mask)
-    L = _lib or lib()
-    if ws is None:
-        ws = topk_idx.new_empty(max(L.moe_balance_workspace_bytes(T, E), 256), dtype=torch.uint8)
-    else:
+    if ws is not None:
         _need("ws", ws, _U8, None, dev)
-    loss = topk_idx.new_empty(2, dtype=torch.float32)
-    counts = topk_idx.new_empty(E)
-    mean_prob = topk_idx.new_empty(E, dtype=torch.float32)
+        ws_ptr, ws_bytes, own = ws.data_ptr(), ws.numel(), 0
+    else:
+        ws_bytes = (_lib or lib()).moe_balance_workspace_bytes(T, E)
+        own = ws_bytes if ws_bytes <= 4096 else 0    # a small workspace lies behind the results
+        if not own:
+            ws = topk_idx.new_empty(max(ws_bytes, 256), dtype=torch.uint8)
+            ws_ptr = ws.data_ptr()
+    # the results share one allocation, each from a 16-byte boundary on
+    pad = -E % 4
+    counts, _, mean_prob, _, loss, _, tail = topk_idx.new_empty(2 * (E + pad) + 4 + own // 4).split_with_sizes(
+        [E, pad, E, pad, 2, 2, own // 4])
+    if own:
+        ws_ptr = tail.data_ptr()
+    mean_prob, loss = mean_prob.view(torch.float32), loss.view(torch.float32)
     _run("moe_balance_loss", dev, logits.data_ptr(), _XTYPES[logits.dtype], T, E, topk_idx.data_ptr(), k,
          None if mask is None else mask.data_ptr(), loss.data_ptr(), counts.data_ptr(), mean_prob.data_ptr(),
-         ws.data_ptr(), ws.numel())
+         ws_ptr, ws_bytes)
     return loss, counts, mean_prob
 
 
