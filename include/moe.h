@@ -306,8 +306,9 @@ moe_status moe_quantize_rows_mx4(const void *v, int32_t xtype, int32_t rows, int
  *           out_scales uint8 [rows][columns/32], as moe_quantize_rows_mx4 on the fp32 result;
  *           out_scales is NULL otherwise.
  * K a multiple of 64, 64 <= K <= 16384; 1 <= N <= 65536; 1 <= E <= 512; 1 <= rows, x_rows <= 2^21;
- * 1 <= k <= 64.  w_scales and x_scales hold 2 K/64 bytes a row.  An infinite fp32 value of x gives
- * NaN in its row's outputs.  out and out_scales overlap none of the inputs.
+ * 1 <= k <= 64; rows * N <= 2^34 (MOE_EUNSUPPORTED beyond).  An infinite fp32 value of x gives NaN in
+ * its row's outputs; with x in fp32 or bf16 a weight beyond the fp32 range (scale byte 254 with codes
+ * of 2 and more) counts as infinite.  out and out_scales overlap none of the inputs.
  */
 moe_status moe_matmul_mx4(const void *x, const uint8_t *x_scales, int32_t xtype, int32_t x_rows, int32_t K,
                           const int32_t *perm, int32_t k, int32_t rows, const uint8_t *w, const uint8_t *w_scales,

@@ -365,7 +365,7 @@ def matmul_mx4(x, w, w_scales, x_scales=None, offsets=None, perm=None, k: int = 
     scales = None
     if out_dtype == torch.uint8:
         if out is None:
-            out = x.new_empty((rows, cols // 2)), x.new_empty((rows, cols // 32))
+            out = (x.new_empty((rows, cols // 2), dtype=torch.uint8), x.new_empty((rows, cols // 32), dtype=torch.uint8))
         codes, scales = out
         _need("out[0]", codes, _U8, (rows, cols // 2), dev)
         _need("out[1]", scales, _U8, (rows, cols // 32), dev)

@@ -589,6 +589,7 @@ moe_status moe_matmul_mx4(const void *x, const uint8_t *x_scales, int32_t xtype,
     if (otype == MOE_X_MX4 ? !aligned16(out_scales) : out_scales != nullptr) return MOE_EINVAL;
     const int columns = act == MOE_ACT_SWIGLU ? N / 2 : N;
     if (otype == MOE_X_MX4 && (xtype != MOE_X_MX4 || columns % MX_BLOCK_VALUES)) return MOE_EUNSUPPORTED;
+    if ((int64_t)rows * N > (int64_t)1 << 34) return MOE_EUNSUPPORTED;   // keeps every grid below 2^32 threads
     Mx4Product p{};
     p.x = x;
     p.xs = x_scales;

@@ -188,11 +188,11 @@ __device__ __forceinline__ Tile find_tile(const Mx4Product &p, int b, int bm, in
     return q.find(p, bm, mine(q.total));
 }
 
-// The `slot`-th group that holds rows, all of its rows (a tile of 2^30 rows holds any group).
-__device__ __forceinline__ Tile find_slot(const Mx4Product &p, int slot, int lane)
+// Tile `tile` of all groups' rows cut into tiles of `bm`.
+__device__ __forceinline__ Tile find_rows(const Mx4Product &p, int tile, int bm, int lane)
 {
-    if (p.offsets == nullptr) return Tile{0, 0, slot == 0 ? p.Pr : 0};
-    return Tiling(p, 1 << 30, lane).find(p, 1 << 30, slot);
+    if (p.offsets == nullptr) return Tile{0, tile * bm, min(bm, p.Pr - tile * bm)};
+    return Tiling(p, bm, lane).find(p, bm, tile);
 }
 
 __device__ __forceinline__ int source_row(const Mx4Product &p, int r)
@@ -565,22 +565,30 @@ __device__ __forceinline__ void lds_dma2(const void *g, uint32_t lds)
 }
 
 // MT: 16-row fragments of x at a time.
-template <int XK, bool GLU, int MT, int KS>
-__global__ __launch_bounds__(64 * PW_WAVES, KS == 1 && MT == 1 ? 3 : 2) void product_wide_kernel(Mx4Product p)
-{
-    constexpr int NTERM = XTerms<XK>::N, SETS = PW_WAVES / KS;
-    __shared__ __attribute__((aligned(16))) uint8_t s_ring[PW_WAVES * PW_RING * PW_STAGE];
+template <int XK, int MT, int KS>
+struct Wide {
     // x: three blocks to a CU where they are many and their groups small, else two
-    constexpr int PW_SLAB = (KS == 1 && MT == 1 ? 16 : 40) * 1024;
+    static constexpr int SLAB = (KS == 1 && MT == 1 ? 16 : 40) * 1024;
+    // rows of a block: as many as KS stages of x fit the slab for
+    static constexpr int FIT = SLAB / (2 * XTerms<XK>::N * (KS * 256 + 8));
+    static constexpr int RM = FIT < 16 * MT ? FIT : 16 * MT;
+};
+
+template <int XK, bool GLU, int MT, int KS>
+__global__ __launch_bounds__(64 * PW_WAVES, KS == 1 && MT == 1 ? 3 : 2) void product_wide_kernel(Mx4Product p, int nblocks)
+{
+    constexpr int NTERM = XTerms<XK>::N, SETS = PW_WAVES / KS, RM = Wide<XK, MT, KS>::RM, PW_SLAB = Wide<XK, MT, KS>::SLAB;
+    __shared__ __attribute__((aligned(16))) uint8_t s_ring[PW_WAVES * PW_RING * PW_STAGE];
     __shared__ __attribute__((aligned(16))) uint8_t s_slab[PW_SLAB];
     __shared__ int s_src[16 * MT];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, li = lane & 15, lg = lane >> 4;
-    const Tile t = find_slot(p, blockIdx.y, lane);
+    const int slot = blockIdx.x / nblocks;
+    const Tile t = find_rows(p, slot, RM, lane);
     if (t.rows < 1) return;
     constexpr int WO = GLU ? 16 : 32, TN = 2;              // outputs of a set, 16-row weight tiles
     const int F = p.N >> 1, NO = GLU ? F : p.N;
     const int KB = p.K >> 1, KSC = p.K >> 5, steps = (p.K + 255) >> 8;   // stages of 256 columns
-    const int ks = wave % KS, n0 = (blockIdx.x * SETS + wave / KS) * WO;
+    const int ks = wave % KS, n0 = ((blockIdx.x - slot * nblocks) * SETS + wave / KS) * WO;
     const bool live = n0 < NO;
     uint8_t *ring = s_ring + wave * PW_RING * PW_STAGE;
     // sources: 8 lanes read a weight row's 128 bytes of a stage; lanes r and r + 32 the scales of row r
@@ -609,170 +617,164 @@ __global__ __launch_bounds__(64 * PW_WAVES, KS == 1 && MT == 1 ? 3 : 2) void pro
         for (int h = 0; h < 2; ++h) lds_dma2(wsc + min(8 * s + 4 * h + ((lane >> 4) & 2), KSC - 2), L + 4096 + 256 * h);
     };
 
-    // rows at a time: as many as KS steps of x fit the slab for
-    constexpr int RM = PW_SLAB / (2 * NTERM * (KS * 256 + 8)) < 16 * MT ? PW_SLAB / (2 * NTERM * (KS * 256 + 8)) : 16 * MT;
+    const int R = t.rows;
+    if (live) issue(ks, 0);
 
-    for (int r0 = 0; r0 < t.rows; r0 += RM) {
-        const int R = min(RM, t.rows - r0);
-        if (live) issue(ks, 0);
-
-        // ---- x: [term][row][columns of a slab + 8]; the slab holds all of K where it fits
-        if (tid < R) s_src[tid] = source_row(p, t.row0 + r0 + tid);
-        const int SC = (PW_SLAB / (2 * NTERM * R) - 8) / 256 / KS * KS;   // stages of a slab, at least KS
-        const int XS = min(SC, steps) * 256 + 8;                   // bf16 values of a slab row
-        const int nslab = (steps + SC - 1) / SC;
-        uint16_t *slab = reinterpret_cast<uint16_t *>(s_slab);
-        auto load_slab = [&](int b) {
-            const int c0 = b * SC * 256, pieces = (min(steps, (b + 1) * SC) * 256 - c0) / 8;
-            for (int i = tid; i < R * pieces; i += 64 * PW_WAVES) {
-                const int r = i / pieces, c = 8 * (i - r * pieces);
-                const size_t at = (size_t)s_src[r] * p.K + c0 + c;
-                const bool in = c0 + c < p.K;
-                uint16_t *dst = slab + r * XS + c;
-                if constexpr (XK == X_F32) {
-                    float v[8] = {};
-                    if (in) {
-                        const float4 *g = reinterpret_cast<const float4 *>(static_cast<const float *>(p.x) + at);
-                        const float4 a = g[0], b4 = g[1];
-                        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-                        v[4] = b4.x; v[5] = b4.y; v[6] = b4.z; v[7] = b4.w;
-                    }
-                    bf16x8 xt[3];
-                    cut_f32x8(v, xt);
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) *reinterpret_cast<bf16x8 *>(dst + k * R * XS) = xt[k];
-                } else {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (in) v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + at);
-                    *reinterpret_cast<uint4 *>(dst) = v;
+    // ---- x: [term][row][columns of a slab + 8]; the slab holds all of K where it fits
+    if (tid < R) s_src[tid] = source_row(p, t.row0 + tid);
+    const int SC = (PW_SLAB / (2 * NTERM * R) - 8) / 256 / KS * KS;   // stages of a slab, at least KS
+    const int XS = min(SC, steps) * 256 + 8;                   // bf16 values of a slab row
+    const int nslab = (steps + SC - 1) / SC;
+    uint16_t *slab = reinterpret_cast<uint16_t *>(s_slab);
+    auto load_slab = [&](int b) {
+        const int c0 = b * SC * 256, pieces = (min(steps, (b + 1) * SC) * 256 - c0) / 8;
+        for (int i = tid; i < R * pieces; i += 64 * PW_WAVES) {
+            const int r = i / pieces, c = 8 * (i - r * pieces);
+            const size_t at = (size_t)s_src[r] * p.K + c0 + c;
+            const bool in = c0 + c < p.K;
+            uint16_t *dst = slab + r * XS + c;
+            if constexpr (XK == X_F32) {
+                float v[8] = {};
+                if (in) {
+                    const float4 *g = reinterpret_cast<const float4 *>(static_cast<const float *>(p.x) + at);
+                    const float4 a = g[0], b4 = g[1];
+                    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+                    v[4] = b4.x; v[5] = b4.y; v[6] = b4.z; v[7] = b4.w;
                 }
+                bf16x8 xt[3];
+                cut_f32x8(v, xt);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) *reinterpret_cast<bf16x8 *>(dst + k * R * XS) = xt[k];
+            } else {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (in) v = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.x) + at);
+                *reinterpret_cast<uint4 *>(dst) = v;
             }
-        };
+        }
+    };
 
-        int buf = 0;
-        // With few rows the three terms of an fp32 x fit side by side: column li of the matrix product
-        // is term li / R of row li % R, one instruction does the work of three, and the columns of a
-        // row are added at the end (8 tokens' down projection 18.5 -> 17.3 us).
-        const bool packed = XK == X_F32 && MT == 1 && 3 * R <= 16;
-        const int xrow = packed ? min(li, 3 * R - 1) : li;
+    int buf = 0;
+    // With few rows the three terms of an fp32 x fit side by side: column li of the matrix product
+    // is term li / R of row li % R, one instruction does the work of three, and the columns of a
+    // row are added at the end (8 tokens' down projection 18.5 -> 17.3 us).
+    const bool packed = XK == X_F32 && MT == 1 && 3 * R <= 16;
+    const int xrow = packed ? min(li, 3 * R - 1) : li;
 
-        f32x4 acc[TN][MT];
+    f32x4 acc[TN][MT];
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+    for (int j = 0; j < TN; ++j)
 #pragma unroll
-            for (int m = 0; m < MT; ++m) acc[j][m] = zero4();
-        for (int b = 0; b < nslab; ++b) {
-            lds_barrier();
-            load_slab(b);
-            lds_barrier();
-            const int send = live ? min(steps, (b + 1) * SC) : 0;
-            for (int s = b * SC + ks; s < send; s += KS) {
-                // this stage has landed, and what was read from the buffer to fill next has arrived
-                asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-                issue(s + KS, buf ^ 1);
-                const uint8_t *W = ring + buf * PW_STAGE;
-                buf ^= 1;
+        for (int m = 0; m < MT; ++m) acc[j][m] = zero4();
+    for (int b = 0; b < nslab; ++b) {
+        lds_barrier();
+        load_slab(b);
+        lds_barrier();
+        const int send = live ? min(steps, (b + 1) * SC) : 0;
+        for (int s = b * SC + ks; s < send; s += KS) {
+            // this stage has landed, and what was read from the buffer to fill next has arrived
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+            issue(s + KS, buf ^ 1);
+            const uint8_t *W = ring + buf * PW_STAGE;
+            buf ^= 1;
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {              // 128 columns
-                    const uint32_t *S = reinterpret_cast<const uint32_t *>(W + 4096) + 64 * u + (lg >> 1) * 32 + li;
-                    uint4 w[TN];
-                    float sc[TN];
+            for (int u = 0; u < 2; ++u) {              // 128 columns
+                const uint32_t *S = reinterpret_cast<const uint32_t *>(W + 4096) + 64 * u + (lg >> 1) * 32 + li;
+                uint4 w[TN];
+                float sc[TN];
 #pragma unroll
-                    for (int j = 0; j < TN; ++j) {
-                        w[j] = *reinterpret_cast<const uint4 *>(W + chunk_at(16 * j + li, 4 * u + lg));
-                        sc[j] = e8m0_f32((S[16 * j] >> (8 * (lg & 1))) & 0xFFu);
-                    }
+                for (int j = 0; j < TN; ++j) {
+                    w[j] = *reinterpret_cast<const uint4 *>(W + chunk_at(16 * j + li, 4 * u + lg));
+                    sc[j] = e8m0_f32((S[16 * j] >> (8 * (lg & 1))) & 0xFFu);
+                }
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        if (MT > 1 && 16 * m >= R) break;
-                        const uint16_t *X = slab + (packed ? xrow : min(16 * m + li, R - 1)) * XS + (s - b * SC) * 256 + 128 * u + 32 * lg;
-                        if (packed) {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const bf16x8 xt = *reinterpret_cast<const bf16x8 *>(X + 8 * q);
-#pragma unroll
-                                for (int j = 0; j < TN; ++j) {
-                                    const uint32_t c = q == 0 ? w[j].x : q == 1 ? w[j].y : q == 2 ? w[j].z : w[j].w;
-                                    acc[j][m] = mfma16x16x32_bf16(mx4_bf16x8(c, sc[j]), xt, acc[j][m]);
-                                }
-                            }
-                            continue;
-                        }
+                for (int m = 0; m < MT; ++m) {
+                    if (MT > 1 && 16 * m >= R) break;
+                    const uint16_t *X = slab + (packed ? xrow : min(16 * m + li, R - 1)) * XS + (s - b * SC) * 256 + 128 * u + 32 * lg;
+                    if (packed) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
-                            bf16x8 xt[NTERM];
-#pragma unroll
-                            for (int k = 0; k < NTERM; ++k) xt[k] = *reinterpret_cast<const bf16x8 *>(X + k * R * XS + 8 * q);
+                            const bf16x8 xt = *reinterpret_cast<const bf16x8 *>(X + 8 * q);
 #pragma unroll
                             for (int j = 0; j < TN; ++j) {
                                 const uint32_t c = q == 0 ? w[j].x : q == 1 ? w[j].y : q == 2 ? w[j].z : w[j].w;
-                                const bf16x8 wb = mx4_bf16x8(c, sc[j]);
-#pragma unroll
-                                for (int k = NTERM - 1; k >= 0; --k) acc[j][m] = mfma16x16x32_bf16(wb, xt[k], acc[j][m]);
+                                acc[j][m] = mfma16x16x32_bf16(mx4_bf16x8(c, sc[j]), xt, acc[j][m]);
                             }
+                        }
+                        continue;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        bf16x8 xt[NTERM];
+#pragma unroll
+                        for (int k = 0; k < NTERM; ++k) xt[k] = *reinterpret_cast<const bf16x8 *>(X + k * R * XS + 8 * q);
+#pragma unroll
+                        for (int j = 0; j < TN; ++j) {
+                            const uint32_t c = q == 0 ? w[j].x : q == 1 ? w[j].y : q == 2 ? w[j].z : w[j].w;
+                            const bf16x8 wb = mx4_bf16x8(c, sc[j]);
+#pragma unroll
+                            for (int k = NTERM - 1; k >= 0; --k) acc[j][m] = mfma16x16x32_bf16(wb, xt[k], acc[j][m]);
                         }
                     }
                 }
             }
         }
-        // no load may still be writing LDS
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (!live) continue;
-        if (packed) {
-            // row r: the small terms first
+    }
+    // no load may still be writing LDS
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (!live) return;
+    if (packed) {
+        // row r: the small terms first
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
+        for (int j = 0; j < TN; ++j)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float mid = __shfl(acc[j][0][i], (lane & 48) | min(li + R, 15), WAVE);
-                    const float low = __shfl(acc[j][0][i], (lane & 48) | min(li + 2 * R, 15), WAVE);
-                    acc[j][0][i] += low + mid;
+            for (int i = 0; i < 4; ++i) {
+                const float mid = __shfl(acc[j][0][i], (lane & 48) | min(li + R, 15), WAVE);
+                const float low = __shfl(acc[j][0][i], (lane & 48) | min(li + 2 * R, 15), WAVE);
+                acc[j][0][i] += low + mid;
+            }
+    }
+    // ---- element i of a lane's acc[j][m] is weight row 16 j + 4 lg + i of x row 16 m + li
+    if constexpr (KS > 1) {
+        // the KS waves' sums meet in LDS, in wave order (the rings are idle)
+        float *red = reinterpret_cast<float *>(ring);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            if (16 * m >= R) break;
+            if (m > 0) lds_barrier();
+#pragma unroll
+            for (int j = 0; j < TN; ++j) *reinterpret_cast<f32x4 *>(red + li * 36 + 16 * j + 4 * lg) = acc[j][m];
+            lds_barrier();
+            const int rows = min(16, R - 16 * m);
+            for (int i = ks * 64 + lane; i < rows * WO; i += KS * 64) {
+                const int r = i / WO, n = i & (WO - 1);
+                const float *q = reinterpret_cast<const float *>(s_ring + (wave - ks) * PW_RING * PW_STAGE) + r * 36 + n;
+                float v = 0.f, u = 0.f;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    v += q[k * (PW_RING * PW_STAGE / 4)];
+                    if (GLU) u += q[k * (PW_RING * PW_STAGE / 4) + 16];
                 }
-        }
-        // ---- element i of a lane's acc[j][m] is weight row 16 j + 4 lg + i of x row 16 m + li
-        if constexpr (KS > 1) {
-            // the KS waves' sums meet in LDS, in wave order (the rings are idle)
-            float *red = reinterpret_cast<float *>(ring);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (16 * m >= R) break;
-                if (m > 0) lds_barrier();
-#pragma unroll
-                for (int j = 0; j < TN; ++j) *reinterpret_cast<f32x4 *>(red + li * 36 + 16 * j + 4 * lg) = acc[j][m];
-                lds_barrier();
-                const int rows = min(16, R - 16 * m);
-                for (int i = ks * 64 + lane; i < rows * WO; i += KS * 64) {
-                    const int r = i / WO, n = i & (WO - 1);
-                    const float *q = reinterpret_cast<const float *>(s_ring + (wave - ks) * PW_RING * PW_STAGE) + r * 36 + n;
-                    float v = 0.f, u = 0.f;
-#pragma unroll
-                    for (int k = 0; k < KS; ++k) {
-                        v += q[k * (PW_RING * PW_STAGE / 4)];
-                        if (GLU) u += q[k * (PW_RING * PW_STAGE / 4) + 16];
-                    }
-                    if (n0 + n < NO) {
-                        v = GLU ? silu_fast(v) * u : activate(v, p.act);
-                        const size_t at = (size_t)(t.row0 + r0 + 16 * m + r) * NO + n0 + n;
-                        if (p.otype == X_F32) store1<X_F32>(p, at, v);
-                        else store1<X_BF16>(p, at, v);
-                    }
+                if (n0 + n < NO) {
+                    v = GLU ? silu_fast(v) * u : activate(v, p.act);
+                    const size_t at = (size_t)(t.row0 + 16 * m + r) * NO + n0 + n;
+                    if (p.otype == X_F32) store1<X_F32>(p, at, v);
+                    else store1<X_BF16>(p, at, v);
                 }
             }
-            lds_barrier();                                 // the sums are read before the rings fill again
-        } else {
+        }
+    } else {
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                if (16 * m + li >= R) continue;
-                const size_t row = (size_t)(t.row0 + r0 + 16 * m + li) * NO;
+        for (int m = 0; m < MT; ++m) {
+            if (16 * m + li >= R) continue;
+            const size_t row = (size_t)(t.row0 + 16 * m + li) * NO;
 #pragma unroll
-                for (int j = 0; j < (GLU ? 1 : 2); ++j) {
-                    const int n = n0 + 16 * j + 4 * lg;
-                    float v[4];
+            for (int j = 0; j < (GLU ? 1 : 2); ++j) {
+                const int n = n0 + 16 * j + 4 * lg;
+                float v[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        v[i] = GLU ? silu_fast(acc[j][m][i]) * acc[1][m][i] : activate(acc[j][m][i], p.act);
-                    store4(p, row + n, n, NO, v);
-                }
+                for (int i = 0; i < 4; ++i)
+                    v[i] = GLU ? silu_fast(acc[j][m][i]) * acc[1][m][i] : activate(acc[j][m][i], p.act);
+                store4(p, row + n, n, NO, v);
             }
         }
     }
@@ -784,16 +786,20 @@ hipError_t launch_wide(const Mx4Product &p, hipStream_t s)
     const int WO = GLU ? 16 : 32, NO = GLU ? p.N / 2 : p.N;
     const int rows = p.Pr + p.S * p.T, G = p.offsets ? p.E + p.S : 1;
     const int slots = rows < G ? rows : G, sets = (NO + WO - 1) / WO;
-    const auto grid = [&](int per) { return dim3((sets + per - 1) / per, slots); };
-    // Where groups hold many rows: 64 (fp32: 20, which the slab holds) at a time, not 16.
+    const auto go = [&](auto kernel, int rm, int per) {
+        const int nblocks = (sets + per - 1) / per;
+        kernel<<<(unsigned)(rows / rm + slots) * nblocks, 64 * PW_WAVES, 0, s>>>(p, nblocks);
+    };
+    // Where groups hold many rows: 64 (fp32: 25, which the slab holds) at a time, not 16.
+    constexpr int MANY = XK == X_F32 ? 2 : 4;
     if (rows > 16 && rows >= 8 * G)
-        product_wide_kernel<XK, GLU, XK == X_F32 ? 2 : 4, 1><<<grid(PW_WAVES), 64 * PW_WAVES, 0, s>>>(p);
+        go(product_wide_kernel<XK, GLU, MANY, 1>, Wide<XK, MANY, 1>::RM, PW_WAVES);
     // Four waves share a set's columns while the sets alone leave the GPU short of waves (256 CUs of
     // 12): one token's 44 sets x 8 experts 9.0 us split and 18 whole, 88 x 51 at 8 tokens 37 and 19.
     else if ((long long)sets * slots < 2048)
-        product_wide_kernel<XK, GLU, 1, PW_WAVES><<<grid(1), 64 * PW_WAVES, 0, s>>>(p);
+        go(product_wide_kernel<XK, GLU, 1, PW_WAVES>, Wide<XK, 1, PW_WAVES>::RM, 1);
     else
-        product_wide_kernel<XK, GLU, 1, 1><<<grid(PW_WAVES), 64 * PW_WAVES, 0, s>>>(p);
+        go(product_wide_kernel<XK, GLU, 1, 1>, Wide<XK, 1, 1>::RM, PW_WAVES);
     return hipGetLastError();
 }
 

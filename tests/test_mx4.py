@@ -82,6 +82,7 @@ def test_matmul_argument_checks():
     assert mm(ot=2, os=FAKE, N=64) == moe.EUNSUPPORTED
     assert mm(xt=2, xs=FAKE, ot=2, os=FAKE, N=48) == moe.EUNSUPPORTED
     assert mm(xt=2, xs=FAKE, ot=2, os=FAKE, N=96, act=0) == moe.EUNSUPPORTED
+    assert mm(rows=1 << 20, N=(1 << 14) + 2) == moe.EUNSUPPORTED         # rows * N > 2^34
 
 
 def test_layer_argument_checks():
@@ -350,6 +351,115 @@ def test_product_of_one_group_without_offsets():
         got = moe.matmul_mx4(x, w[0], ws[0], x_scales=xs, out_dtype=torch.float32)
         torch.cuda.synchronize()
         np.testing.assert_array_equal(f64(got), xv @ ref.decode(w[0].cpu(), ws[0].cpu()).T)
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["mx4", "bf16", "f32"])
+def test_product_at_the_ends_of_the_scales(kind):
+    """Scale bytes from 1 to 253, and 0 and 254 with codes that stay in range, against rows that bring
+    the products back: every sum here has one nonzero term per block pair, exact in fp32."""
+    K, N = 256, 48
+    w = torch.zeros((1, N, K // 2), dtype=torch.uint8)
+    ws = torch.full((1, N, K // 32), 127, dtype=torch.uint8)
+    e = torch.linspace(-126, 126, N).round().int()
+    w[0, :, 0], ws[0, :, 0] = 0x02, (e + 127).to(torch.uint8)          # 1 x 2^e at column 0
+    w[0, 0, 0], ws[0, 0, 0] = 0x02, 254                                # 2^127
+    w[0, 1, 0], ws[0, 1, 0] = 0x07, 0                                  # 6 x 2^-127, normal in fp32
+    x = torch.zeros((3, K))
+    x[:, 0] = torch.tensor([1.0, -1.5, 2.0]) * torch.tensor([1.0, 2.0 ** -10, 2.0 ** 10])
+    xs = None
+    if kind == "mx4":
+        q, s = ref.quantize(x.double().numpy())
+        x, xs = torch.from_numpy(q).to(DEV), torch.from_numpy(s).to(DEV)
+        xv = ref.decode(q, s)
+    else:
+        xv = x.double().numpy()
+        x = x.to(torch.bfloat16 if kind == "bf16" else torch.float32).to(DEV)
+    want = xv @ ref.decode(w[0], ws[0]).T
+    got = f64(moe.matmul_mx4(x, w.to(DEV), ws.to(DEV), x_scales=xs, out_dtype=torch.float32))
+    normal = (np.abs(want) >= 2.0 ** -126) & (np.abs(want) < 2.0 ** 128)
+    assert normal.sum() > 120
+    np.testing.assert_array_equal(got[normal], want[normal])
+    assert np.abs(got[np.abs(want) < 2.0 ** -126]).max() <= 2.0 ** -126   # below: flushed or kept
+
+
+@gpu
+@pytest.mark.parametrize("kind", ["mx4", "bf16"])
+def test_product_past_32_bit_offsets(kind):
+    """Outputs of over 2^32 bytes, and weights of over 2^32 bytes: the last rows and the last group."""
+    K = 64
+    rows, N = 1 << 19, 2304                                             # 4.8 GB of fp32
+    w, ws = make_w(2, N, K, 1, 1)
+    x, xs, xv = make_x(kind, rows, K, 1, 1, True)
+    off = torch.tensor([0, 1000, rows], dtype=torch.int32, device=DEV)
+    got = moe.matmul_mx4(x, w, ws, x_scales=xs, offsets=off, out_dtype=torch.float32)
+    at = np.r_[0:3, 998:1003, rows // 2:rows // 2 + 3, rows - 5:rows]
+    wv = ref.decode(w.cpu(), ws.cpu())
+    want = np.stack([xv[r] @ wv[0 if r < 1000 else 1].T for r in at])
+    np.testing.assert_array_equal(f64(got[torch.from_numpy(at).to(DEV)]), want)
+    del got, x
+    K, N, E = 16384, 8192, 70                                           # 4.7 GB of codes
+    w = torch.zeros((E, N, K // 2), dtype=torch.uint8, device=DEV)
+    ws = torch.full((E, N, K // 32), 127, dtype=torch.uint8, device=DEV)
+    w1, ws1 = make_w(1, N, K, 2, 1)
+    w[-1], ws[-1] = w1[0], ws1[0]
+    x, xs, xv = make_x(kind, 3, K, 3, 1, True)
+    off = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    off[-1] = 3
+    got = moe.matmul_mx4(x, w, ws, x_scales=xs, offsets=off, out_dtype=torch.float32)
+    np.testing.assert_array_equal(f64(got), xv @ ref.decode(w1[0].cpu(), ws1[0].cpu()).T)
+
+
+@gpu
+def test_product_on_a_side_stream_of_its_own_inputs():
+    """Two products at once on two streams, each with its own inputs and outputs."""
+    E, N, K, rows = 8, 512, 1024, 400
+    args, want = [], []
+    for i, kind in enumerate(("mx4", "bf16")):
+        w, ws = make_w(E, N, K, i, 3)
+        x, xs, _ = make_x(kind, rows, K, i, 3, False)
+        args.append((x, w, ws, xs, torch.from_numpy(make_groups(E, rows, i, "even")).to(DEV)))
+        x, w, ws, xs, off = args[-1]
+        want.append(moe.matmul_mx4(x, w, ws, x_scales=xs, offsets=off))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in args]
+    got = [[], []]
+    for _ in range(6):
+        for i, s in enumerate(streams):
+            x, w, ws, xs, off = args[i]
+            with torch.cuda.stream(s):
+                got[i].append(moe.matmul_mx4(x, w, ws, x_scales=xs, offsets=off))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+
+
+@gpu
+def test_refusals_on_the_gpu():
+    w, ws = make_w(2, 64, 128, 0, 1)
+    x = torch.zeros((4, 128), dtype=torch.bfloat16, device=DEV)
+    off = torch.tensor([0, 2, 4], dtype=torch.int32, device=DEV)
+    ok = dict(offsets=off)
+    assert moe.matmul_mx4(x, w, ws, **ok).shape == (4, 64)
+    for bad in (dict(offsets=None), dict(offsets=off.long()), dict(offsets=off[:2].contiguous()), dict(offsets=off.cpu()),
+                dict(ok, perm=off.long()), dict(ok, perm=off[:, None]), dict(ok, x_scales=ws), dict(ok, out_dtype=torch.float16),
+                dict(ok, out=torch.zeros((4, 63), dtype=torch.bfloat16, device=DEV)),
+                dict(ok, out=torch.zeros((64, 4), dtype=torch.bfloat16, device=DEV).T)):
+        with pytest.raises((TypeError, ValueError)):
+            moe.matmul_mx4(x, w, ws, **bad)
+    for bad in (dict(ok, act=7), dict(ok, k=3), dict(ok, out_dtype=torch.uint8)):
+        with pytest.raises(moe.MoeError):
+            moe.matmul_mx4(x, w, ws, **bad)
+    with pytest.raises(ValueError):
+        moe.matmul_mx4(x[:, ::2], w, ws, **ok)                 # strided, and too short
+    with pytest.raises(ValueError):
+        moe.quantize_rows_mx4(x.T)
+    with pytest.raises(moe.MoeError):
+        moe.quantize_rows_mx4(x[:, :96].contiguous())          # not a multiple of 64
+    with pytest.raises(moe.MoeError):
+        moe.quantize_rows_mx4(x[:0])                           # no rows
+    with pytest.raises(moe.MoeError):
+        moe.matmul_mx4(x.view(-1)[4:388].view(3, 128), w[0], ws[0])   # 8 bytes off a 16-byte boundary
 
 
 # ------------------------------------------------------------------------------------------
