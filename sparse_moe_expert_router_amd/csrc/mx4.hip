@@ -248,19 +248,29 @@ __device__ __forceinline__ void store4(const Mx4Product &p, size_t at, int n, in
 }
 
 // ---------------------------------------------------------------------------------------------
-// Product of MX4 rows.  A block of 4 waves computes BM = 128 rows by BN = 256 weight rows (128 gate
-// rows and their 128 up rows with SwiGLU); wave w owns 64 of the weight rows and all 128 rows.
-// Weights are the A operand (their rows become 4 consecutive outputs of a lane), x the B operand.
+// Product of MX4 rows.  A block of 4 waves computes up to 160 rows by 256 weight rows (128 gate rows
+// and their 128 up rows with SwiGLU); wave w owns 64 of the weight rows and all the rows.  Weights are
+// the A operand (their rows become 4 consecutive outputs of a lane), x the B operand.
+//
 // An MFMA lane holds one row's 16 bytes, so neighbouring lanes hold different rows: loaded straight
-// into registers, every lane would be a cache access of its own (64 per KB).  Both operands
-// therefore go through LDS by direct-to-LDS loads whose neighbouring lanes read neighbouring bytes
-// (16 accesses per KB), double-buffered in stages of 128 columns.
+// into registers, every lane would be a cache access of its own (64 per KB; gate/up of 2048 tokens 206
+// us that way).  Both operands therefore go through LDS by direct-to-LDS loads whose neighbouring
+// lanes read neighbouring bytes, in stages of 128 columns.  E2M1 products run at twice the rate in the
+// 32x32x64 form (measured 9.1 PFLOP/s on registers alone) than in the 16x16x128 one (4.8).
+//
+// Measured: gate/up of 2048 tokens top-8 of 128 experts (1408 x 2816) 96 us, 2.8 TB/s of weights and
+// 1.35 PFLOP/s; their down projection (2816 x 704, fp32 out) 102 us, half of it the 185 MB of results
+// and a third a block's way to its first product; 4096 x 6144 x 6144 114 us, 2.7 PFLOP/s.  A copy
+// without loads ran the first in 69 and the last in 84 us: what is left is latency at a block's start
+// and the operands' way from L2 (about 17 bytes a cycle and CU), which the two blocks of a CU hide in
+// part.  Tried and slower: 128 weight rows (162 / 233 / 164 us), four such blocks a CU (200 / 272 /
+// 205), stages through registers (123 / 112 / 133 against 112 / 106 / 130 then).
 
-constexpr int PB_M = 128, PB_N = 256;                  // rows, weight rows of a block
+constexpr int PB_M = 160, PB_N = 256;                  // rows, weight rows of a block
 constexpr int PB_XST = PB_M * 64, PB_WST = PB_N * 64;  // bytes of a stage's codes (128 columns)
 constexpr int PB_XBUF = 2, PB_WBUF = 3;                // weights come from HBM, rows mostly from L2
 constexpr int PB_WLOADS = 4;                           // load instructions of a wave per weight stage
-constexpr int PB_SST = 16 * (PB_M + PB_N);             // 16 scales (512 columns) of every row
+constexpr int PB_SST = 8 * (PB_M + PB_N);              // 8 scales (256 columns) of every row
 constexpr int PB_LDS = PB_WBUF * PB_WST + PB_XBUF * PB_XST + 2 * PB_SST;
 
 __device__ __forceinline__ void lds_dma16(const void *g, uint32_t lds)
@@ -346,23 +356,25 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
         const uint32_t L = lds_addr(xlds + (s & 1) * PB_XST);
         const int off = min(s * 64 + dchunk, KB - 16);
 #pragma unroll
-        for (int i = 0; i < XI; ++i) lds_dma16(xsrc[i] + off, L + (wave + 4 * i) * 1024);
+        for (int i = 0; i < XI; ++i)
+            if (wave + 4 * i < 2 * MG) lds_dma16(xsrc[i] + off, L + (wave + 4 * i) * 1024);
     };
     // the weights need only the group: they are on their way while the rows' places are looked up
     issue_w(0, 0);
     issue_w(1, 1);
-    // thread r: the scales of weight row r and (the first 128) of row r
+    // thread r: the scales of weight row r and (the first 160) of row r
     const uint8_t *wsc = p.ws + weight_row(tid) * KSC;
     uint4 sw = scales16(wsc, 0, KSC);
 #pragma unroll
     for (int i = 0; i < XI; ++i) xsrc[i] = static_cast<const uint8_t *>(p.x) + x_row(16 * (wave + 4 * i) + drow) * KB;
     issue_x(0);
-    const uint8_t *xsc = p.xs + x_row(tid & (PB_M - 1)) * KSC;
+    const uint8_t *xsc = p.xs + x_row(min(tid, PB_M - 1)) * KSC;
     uint4 sx = scales16(xsc, 0, KSC);
-    auto put_scales = [&](int q, const uint4 &w, const uint4 &x) {
-        uint4 *S = reinterpret_cast<uint4 *>(slds + (q & 1) * PB_SST);
-        S[tid] = w;
-        if (tid < PB_M) S[PB_N + tid] = x;
+    // columns 256 q ..: two steps' scales of every row
+    auto put_scales = [&](int q, uint32_t w0, uint32_t w1, uint32_t x0, uint32_t x1) {
+        uint2 *S = reinterpret_cast<uint2 *>(slds + (q & 1) * PB_SST);
+        S[tid] = make_uint2(w0, w1);
+        if (tid < PB_M) S[PB_N + tid] = make_uint2(x0, x1);
     };
 
     f32x16v acc[2][MG];
@@ -377,13 +389,13 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
     // its half, byte 2 u is the one.
     auto step = [&](int s, int buf) {
         const uint8_t *X = xlds + (s & 1) * PB_XST, *W = lds + buf * PB_WST + wave * 4096;
-        const uint32_t *S = reinterpret_cast<const uint32_t *>(slds + ((s >> 2) & 1) * PB_SST) + (s & 3) + 4 * li;
-        const uint32_t *WS = S + 256 * wave, *XS = S + 4 * PB_N;
+        const uint32_t *S = reinterpret_cast<const uint32_t *>(slds + ((s >> 1) & 1) * PB_SST) + (s & 1) + 2 * li;
+        const uint32_t *WS = S + 128 * wave, *XS = S + 2 * PB_N;
         int sa[2], sb[MG];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) sa[j] = (int)(WS[128 * j] >> (8 * lh));
+        for (int j = 0; j < 2; ++j) sa[j] = (int)(WS[64 * j] >> (8 * lh));
 #pragma unroll
-        for (int f = 0; f < MG; ++f) sb[f] = (int)(XS[128 * f] >> (8 * lh));
+        for (int f = 0; f < MG; ++f) sb[f] = (int)(XS[64 * f] >> (8 * lh));
         i32x8v a[2][2], b[2][MG];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -406,25 +418,27 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
 
     // Weights are asked for two steps ahead, x one step ahead.  At the top of step s the newest
     // loads in flight are the weights of step s + 1; everything older has to be there.  Every step
-    // issues the same number of loads (past the end the last step's again), so the count holds.
-    // Scales go through registers, 16 of a row at a time: asked for at the first of four steps, put
-    // into the other LDS buffer at the last.
-    put_scales(0, sw, sx);
+    // issues the same number of weight loads (past the end the last step's again), so the count
+    // holds.  Scales go through registers, four steps' of a row at a time, and from there into LDS two
+    // steps' at a time, into the buffer that is not being read.
+    put_scales(0, sw.x, sw.y, sx.x, sx.y);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     int buf = 0;
     for (int s = 0; s < steps; ++s) {
         // stage s has landed in every wave, and every wave has left the buffers filled next
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(PB_WLOADS) : "memory");
-        const int q = (s >> 2) + 1;
-        const bool more = 16 * q < KSC;
-        if ((s & 3) == 0 && more) {
-            sw = scales16(wsc, q, KSC);
-            sx = scales16(xsc, q, KSC);
+        const int q = (s >> 1) + 1;                       // the next two steps
+        if ((s & 3) == 1 && s + 1 < steps) {
+            put_scales(q, sw.z, sw.w, sx.z, sx.w);
+            if (s + 3 < steps) {
+                sw = scales16(wsc, (s >> 2) + 1, KSC);
+                sx = scales16(xsc, (s >> 2) + 1, KSC);
+            }
         }
         if (s + 1 < steps) issue_x(s + 1);
         issue_w(s + 2, buf == 0 ? 2 : buf - 1);
         if (live) step(s, buf);
-        if ((s & 3) == 3 && more) put_scales(q, sw, sx);
+        if ((s & 3) == 3 && s + 1 < steps) put_scales(q, sw.x, sw.y, sx.x, sx.y);
         buf = buf == 2 ? 0 : buf + 1;
     }
     // no load may still be writing LDS, and every wave is done reading it
@@ -500,17 +514,18 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
 }
 
 template <bool GLU, int OT>
-__global__ __launch_bounds__(256, 2) void product_mx4_kernel(Mx4Product p, int ntiles)
+__global__ __launch_bounds__(256, 2) void product_mx4_kernel(Mx4Product p, int bm, int ntiles)
 {
     __shared__ __attribute__((aligned(16))) uint8_t mx4_lds[PB_LDS];
     int nt;
-    const Tile t = find_tile(p, blockIdx.x, PB_M, ntiles, threadIdx.x & 63, nt);
+    const Tile t = find_tile(p, blockIdx.x, bm, ntiles, threadIdx.x & 63, nt);
     if (t.rows < 1) return;
     switch ((t.rows + 31) >> 5) {
     case 1: product_tile<GLU, OT, 1>(p, t, nt, mx4_lds); break;
     case 2: product_tile<GLU, OT, 2>(p, t, nt, mx4_lds); break;
     case 3: product_tile<GLU, OT, 3>(p, t, nt, mx4_lds); break;
-    default: product_tile<GLU, OT, 4>(p, t, nt, mx4_lds); break;
+    case 4: product_tile<GLU, OT, 4>(p, t, nt, mx4_lds); break;
+    default: product_tile<GLU, OT, 5>(p, t, nt, mx4_lds); break;
     }
 }
 
@@ -838,10 +853,15 @@ hipError_t launch_product_mx4(const Mx4Product &p, hipStream_t s)
     const int per = p.act == ACT_SWIGLU ? PB_N / 2 : PB_N;
     const int ntiles = (NO + per - 1) / per;
     const int rows = p.Pr + p.S * p.T, G = p.offsets ? p.E + p.S : 1;
-    const int mtiles = rows / PB_M + (rows < G ? rows : G);        // at least the sum of the groups' tiles
+    // Groups of about a tile's size lie whole in one of 160 rows where 128 would leave many a second
+    // tile of a few rows that reads all the weights again (groups of 128 +- 11 rows, gate/up of 2048
+    // tokens: 96 us against 110).  Larger groups are cut into 128s (4096 rows by 6144 by
+    // 6144: 114 us against 130).
+    const int slots = rows < G ? rows : G, bm = rows <= 144 * slots ? PB_M : 128;
+    const int mtiles = rows / bm + slots;                          // at least the sum of the groups' tiles
     const unsigned grid = ((unsigned)mtiles * ntiles + 7) / 8 * 8;
     const bool glu = p.act == ACT_SWIGLU;
-    auto go = [&](auto g, auto o) { product_mx4_kernel<g.value, o.value><<<grid, 256, 0, s>>>(p, ntiles); };
+    auto go = [&](auto g, auto o) { product_mx4_kernel<g.value, o.value><<<grid, 256, 0, s>>>(p, bm, ntiles); };
     auto by_out = [&](auto g) {
         if (p.otype == X_F32) go(g, std::integral_constant<int, X_F32>{});
         else if (p.otype == X_BF16) go(g, std::integral_constant<int, X_BF16>{});
