@@ -259,8 +259,8 @@ __device__ __forceinline__ void store4(const Mx4Product &p, size_t at, int n, in
 // 32x32x64 form (measured 9.1 PFLOP/s on registers alone) than in the 16x16x128 one (4.8).
 //
 // Measured: gate/up of 2048 tokens top-8 of 128 experts (1408 x 2816) 96 us, 2.8 TB/s of weights and
-// 1.35 PFLOP/s; their down projection (2816 x 704, fp32 out) 102 us, half of it the 185 MB of results
-// and a third a block's way to its first product; 4096 x 6144 x 6144 114 us, 2.7 PFLOP/s.  A copy
+// 1.35 PFLOP/s; their down projection (2816 x 704, fp32 out) 99 us, half of it the 185 MB of results
+// and a third a block's way to its first product; 4096 x 6144 x 6144 112 us, 2.8 PFLOP/s.  A copy
 // without loads ran the first in 69 and the last in 84 us: what is left is latency at a block's start
 // and the operands' way from L2 (about 17 bytes a cycle and CU), which the two blocks of a CU hide in
 // part.  Tried and slower: 128 weight rows (162 / 233 / 164 us), four such blocks a CU (200 / 272 /
@@ -447,7 +447,9 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
 
     // ---- epilogue: lane l, element i of acc[j][f] is output 32 j + 8 (i / 4) + 4 (l / 32) + i % 4 of row
     // 32 f + l % 32.  Each fragment's 32 rows turn round in the wave's own part of LDS, so that
-    // neighbouring lanes store neighbouring outputs of a row.
+    // neighbouring lanes store neighbouring outputs of a row; fp32 and bf16 results with the
+    // non-temporal hint, so that they do not push operands out of L2 that other blocks read again (185
+    // MB of fp32 results 105 -> 99 us, 50 MB of bf16 115 -> 112 us).
     constexpr int RS = WO + 4;
     float *T = reinterpret_cast<float *>(lds) + wave * 32 * (64 + 4);
     const bool whole = NO % (OT == X_F32 ? 4 : 8) == 0;
@@ -476,7 +478,8 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
             for (int i = 0; i < 32 * WO / 4; i += 64) {
                 const int r = (i + lane) / (WO / 4), n = 4 * ((i + lane) & (WO / 4 - 1));
                 const f32x4 v = *reinterpret_cast<const f32x4 *>(T + r * RS + n);
-                if (r < rn && n0 + n < NO) *reinterpret_cast<f32x4 *>(static_cast<float *>(p.out) + (size_t)(r0 + r) * NO + n0 + n) = v;
+                if (r < rn && n0 + n < NO)
+                    __builtin_nontemporal_store(v, reinterpret_cast<f32x4 *>(static_cast<float *>(p.out) + (size_t)(r0 + r) * NO + n0 + n));
             }
         } else {
 #pragma unroll
@@ -492,7 +495,7 @@ __device__ __forceinline__ void product_tile(const Mx4Product &p, const Tile &t,
                     b8 o;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) o[k] = (__bf16)u[k];
-                    if (in) *reinterpret_cast<b8 *>(static_cast<uint16_t *>(p.out) + at) = o;
+                    if (in) __builtin_nontemporal_store(o, reinterpret_cast<b8 *>(static_cast<uint16_t *>(p.out) + at));
                 } else {
                     // four lanes hold a block of 32 outputs
                     uint32_t m = 0;
