@@ -6,7 +6,11 @@
 //     balance = E sum_e f_e P_e,     z = mean_t lse(l_t)^2,
 //     d l_te  = p_te (g_b E / n (f_e - sum_j f_j p_tj) + g_z 2 / n lse_t)
 //             + [e in S_t] w_te (dw_te - sum_j w_tj dw_tj)          (renormalised top-k weights),
-// f taken as a constant (it is a count).  Bound by reading the logits once.
+// f taken as a constant (it is a count).  The floor is reading the logits once (and writing the
+// gradient): 17 MB and 37 MB for 32768 tokens of 128 experts, 4 and 8 us.  Measured there: the loss 10.3
+// + 4.3 us (128 blocks of 16 waves, bound by their arithmetic and the rows' exchanges; then one block
+// that adds up), the gradient 13.8 us, 2.7 TB/s.  A batch of 8 tokens takes one launch of 3.2 us.  The
+// first form (256-thread blocks, no row ahead, library exp and log) took 40 + 6.8 and 16 us.
 //
 // A row's E logits lie in LPR lanes (a power of two) with NJ pieces of VEC values each: softmax
 // needs only exchanges inside those lanes, and the per-expert sums stay in registers until a

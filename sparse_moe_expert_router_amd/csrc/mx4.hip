@@ -20,7 +20,9 @@ namespace {
 // ---------------------------------------------------------------------------------------------
 // Quantiser.  Blocks of 32 lie one after another in memory whatever the row, so the matrix is cut
 // into pieces of 8 values: a lane loads one, the block's largest magnitude is exchanged within
-// four lanes, and each lane writes its 4 bytes of codes.  Bound by memory.
+// four lanes, and each lane writes its 4 bytes of codes.  Bound by memory: 16384 x 704 fp32 with the
+// values 16.5 us, 98 MB at 5.9 TB/s (a copy of the same device reaches 4.65); a single row 1.3 us, a
+// launch.  Two or four pieces a thread changed nothing.
 
 template <typename XT, bool VALUES>
 __global__ __launch_bounds__(256) void quantize_mx4_kernel(const XT *__restrict__ v, long long pieces,
@@ -534,10 +536,15 @@ __global__ __launch_bounds__(256, 2) void product_mx4_kernel(Mx4Product p, int b
 
 // ---------------------------------------------------------------------------------------------
 // Product of bf16 / fp32 rows with MX4 weights: few rows per group, so streaming the weights is what
-// counts.  A wave owns a set of 32 weight rows (with SwiGLU 16 gate rows and their up rows), or with
+// counts.  Measured: 16 tokens top-22 of 512 experts (2688 x 1024) 78 us, 377 MB at 4.8 TB/s; 8 tokens'
+// fp32 rows through 51 experts' down projection (2816 x 704) 17 us; one token's gate/up through 8
+// experts (1408 x 2816) 9 us, which is a block's chain of loads: the groups' offsets, the row's place,
+// the row, while the weights come (weights straight into the matrix cores' lanes: 302 / 66 / 11.5 us).
+//
+// A wave owns a set of 32 weight rows (with SwiGLU 16 gate rows and their up rows), or with
 // KS > 1 every KS-th stage of 256 columns of one, and streams their codes and scales through a ring
-// of its own in LDS by direct-to-LDS loads (neighbouring lanes read neighbouring bytes; straight into
-// the matrix cores' lanes every lane would be a cache access of its own).  Only its own loads fill
+// of its own in LDS by direct-to-LDS loads: neighbouring lanes read neighbouring bytes, whole 128-byte
+// lines of a row, since a second load of a line that is still on its way stalls the cache.  Only its own loads fill
 // the ring, so it runs without barriers.  The group's rows of x lie in LDS for all sets and waves of
 // the block, as bf16: an fp32 x is cut into three terms whose sum is x, weights widen exactly, so
 // every product is exact and the sums are fp32.
