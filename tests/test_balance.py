@@ -318,3 +318,26 @@ def test_replays_in_a_graph_and_on_another_stream():
             g.replay()
             torch.cuda.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(want, got)), i
+
+
+@gpu
+def test_two_batches_at_once():
+    """Losses and gradients of two batches on two streams, each call with a workspace of its own."""
+    batches = [batch(3000, 128, 8, torch.float32), batch(700, 250, 5, torch.float32, seed=1)]
+    dl = torch.tensor([.5, .25], device=DEV)
+
+    def step(b):
+        l, idx, w, dw, _ = b
+        loss, counts, P = moe.balance_loss(l, idx)
+        return loss, counts, P, moe.balance_loss_backward(l, idx, counts, dl, topk_w=w, d_topk_w=dw)
+
+    want = [step(b) for b in batches]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in batches], [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(step(batches[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for g in got[i] for a, b in zip(g, want[i]))

@@ -547,6 +547,42 @@ def test_prefill_layer_near_the_exact_layer():
 
 
 @gpu
+@pytest.mark.parametrize("name,T,act", [("gemma_decode", 8, mi.ACT_SWIGLU), ("gemma_prefill", 300, mi.ACT_SWIGLU),
+                                        ("nemotron_latent", 4, mi.ACT_RELU2)])
+def test_full_size_layers(name, T, act):
+    """Whole layers of the benchmarked shapes on a few of their tokens: exact x and h to the decode bar;
+    with MX4 rows, h within its rounding of the exact one (at most 1 step of the block, 2 where a value
+    above 6 saturates), and the output that of the rounded h (fp32 sums: 1e-5 of the largest output)."""
+    w = mi.workload(name, T=T, fmt=mi.FMT_MX4)
+    lay = mi.make_layer(w, 0, DEV)
+    x, ex, k = mi.make_x(w, 0, device=DEV), lay["experts"], w.k
+    out, idx, wts = moe.layer_forward(x, lay["w_router"], lay["bias"], ex, k, act, want_routing=True)
+    outq = moe.layer_forward(x, lay["w_router"], lay["bias"], ex, k, act, moe.F_PREFILL_MX4)
+    _, off, perm, inv = moe.permute(idx, w.E)
+    q, qs = moe.quantize_rows_mx4(x)
+    hq, hs = moe.matmul_mx4(q, ex["gate_up"], ex["gate_up_scales"], x_scales=qs, offsets=off, perm=perm, k=k, act=act,
+                            out_dtype=torch.uint8)
+    torch.cuda.synchronize()
+    hv = ref.decode(hq.cpu(), hs.cpu())[inv.cpu().numpy()].reshape(T, k, -1)
+    step = np.ldexp(1.0, hs.cpu().numpy().astype(int) - 127).repeat(32, 1)[inv.cpu().numpy()].reshape(T, k, -1)
+    xv, xqv = f64(x), ref.decode(q.cpu(), qs.cpu())
+    a = "swiglu" if act == mi.ACT_SWIGLU else "relu2"
+    for t in sorted({0, T // 2, T - 1}):
+        want, wantq = np.zeros(w.d_model), np.zeros(w.d_model)
+        for j, e in enumerate(idx[t].tolist()):
+            gu = ref.decode(ex["gate_up"][e].cpu(), ex["gate_up_scales"][e].cpu())
+            dn = ref.decode(ex["down"][e].cpu(), ex["down_scales"][e].cpu())
+            want += float(wts[t, j]) * (dn @ ref.activate(gu @ xv[t], a))
+            h = ref.activate(gu @ xqv[t], a)
+            assert (np.abs(hv[t, j] - h) <= 2 * step[t, j] * (1 + 1e-5)).all()
+            small = np.abs(h) <= 6 * step[t, j]
+            assert (np.abs(hv[t, j] - h)[small] <= step[t, j][small] * (1 + 1e-5)).all()
+            wantq += float(wts[t, j]) * (dn @ hv[t, j])
+        assert np.abs(f64(out[t]) - want).max() <= 1e-4 * np.abs(want).max()
+        assert np.abs(f64(outq[t]) - wantq).max() <= 1e-5 * np.abs(wantq).max()
+
+
+@gpu
 def test_intermediates_of_mx4_experts():
     T, E, k, d, dff = 9, 8, 2, 128, 192
     w, lay, x = layer_case(T, E, k, d, dff, mi.ACT_SWIGLU)
